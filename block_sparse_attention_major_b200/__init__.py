@@ -14,9 +14,12 @@ Entry points (same names as the C ABI in include/bsa.h):
     sparse_attn_fwd_token(g, qt, kt, vt, mask, kv_count, dense, token_radius)
                                     the same under a token-level circular support
     forward(g, p, q, k, v, difficulty)       the whole path, raster in, raster out
+    layer_norm_fwd(x, weight, bias)          -> (y, mean, rstd), over the last axis
+    layer_norm_bwd(x, dy, mean, rstd, weight)    -> (dx, dweight, dbias)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -43,6 +46,12 @@ class bsa_mask_params(ctypes.Structure):
     _fields_ = [("window_kind", ctypes.c_int), ("radius", ctypes.c_int), ("topk", ctypes.c_int),
                 ("dense_fraction", ctypes.c_float), ("budget_mode", ctypes.c_int),
                 ("budget_target", ctypes.c_float)]
+
+
+class bsa_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("C", ctypes.c_int), ("items", ctypes.c_int),
+                ("w_per_item", ctypes.c_int), ("x_type", ctypes.c_int), ("y_type", ctypes.c_int),
+                ("w_type", ctypes.c_int), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
 
 
 class BsaError(RuntimeError):
@@ -96,6 +105,13 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.bsa_sparse_attn_fwd_fixed_scratch.restype = ctypes.c_int
         lib.bsa_sparse_attn_fwd_fixed_scratch.argtypes = [G, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp,
                                                           vp, vp]
+        N = ctypes.POINTER(bsa_norm_shape)
+        lib.bsa_layer_norm_fwd.restype = ctypes.c_int
+        lib.bsa_layer_norm_fwd.argtypes = [N] + [vp] * 7
+        lib.bsa_layer_norm_workspace_bytes.restype = sz
+        lib.bsa_layer_norm_workspace_bytes.argtypes = [N]
+        lib.bsa_layer_norm_bwd.restype = ctypes.c_int
+        lib.bsa_layer_norm_bwd.argtypes = [N] + [vp] * 9 + [sz, vp]
         lib.bsa_launch_count.restype = ctypes.c_uint64
         lib.bsa_launch_count.argtypes = []
         lib.bsa_selftest_bounded_wait.restype = ctypes.c_int
@@ -433,6 +449,124 @@ def sparse_attn_fwd_fixed_scratch(g: Geometry, qt: torch.Tensor, kt: torch.Tenso
              ctypes.byref(g.c()), _ptr(qt), _ptr(kt), _ptr(vt), _ptr(mask), _ptr(kv_count),
              ctypes.c_float(sc), _ptr(out), _ptr(lse), _ptr(kernel_errors), s))
     return out, lse
+
+
+_NORM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _owned_by(stream):
+    """Allocations inside belong to `stream` (the current one if None): memory that only the
+    call's own stream touches may then be freed, and reused there, as soon as the call returns."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _norm_shape(x, y_dtype, weight, bias, eps, weight_offset) -> bsa_norm_shape:
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dtype not in _NORM_TYPES or y_dtype not in _NORM_TYPES:
+        raise ValueError(f"x and y must be bfloat16 or float32, got {x.dtype} and {y_dtype}")
+    if x.dim() < 1 or x.numel() == 0 or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous [..., C] tensor with at least one row, got {tuple(x.shape)}")
+    C = x.shape[-1]
+    f = bsa_norm_shape(x.numel() // C, C, 1, 0, _NORM_TYPES[x.dtype], _NORM_TYPES[y_dtype], 1, float(eps),
+                       float(weight_offset))
+    if weight is None:
+        if bias is not None:
+            raise ValueError("a bias needs a weight of the same shape")
+        return f
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in _NORM_TYPES:
+        raise ValueError("weight must be a bfloat16 or float32 tensor")
+    shared, per_item = tuple(weight.shape) == (C,), x.dim() >= 2 and tuple(weight.shape) == (x.shape[0], C)
+    if not shared and not per_item:
+        raise ValueError(f"weight must have shape {(C,)}, or {(x.shape[0], C)} for one per batch item, "
+                         f"got {tuple(weight.shape)}")
+    _need(weight, weight.dtype, weight.shape, "weight")
+    if bias is not None:
+        _need(bias, weight.dtype, weight.shape, "bias")
+    f.w_type = _NORM_TYPES[weight.dtype]
+    if not shared:
+        f.w_per_item, f.items = 1, x.shape[0]
+    return f
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                   eps: float = 1e-6, weight_offset: float = 0.0, out_dtype: torch.dtype | None = None,
+                   y: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                   rstd: torch.Tensor | None = None, want_stats: bool = True,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor | None]:
+    """Layer norm over the last axis of x [..., C] (bfloat16 or float32).
+
+    weight, bias: absent, [C], or [x.shape[0], C] (one row per batch item, as the modulation of
+    a diffusion transformer; weight_offset=1 where it is stored as the distance from one).
+    Returns y (out_dtype, x's type unless given) and the fp32 mean and rstd of every row for
+    the backward pass (None without want_stats)."""
+    dt = y.dtype if y is not None and out_dtype is None else out_dtype or getattr(x, "dtype", None)
+    f = _norm_shape(x, dt, weight, bias, eps, weight_offset)
+    with _owned_by(stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=dt, device=x.device)
+        if want_stats and mean is None:
+            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        if want_stats and rstd is None:
+            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _need(y, dt, x.shape, "y")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _need(t, torch.float32, x.shape[:-1], name)
+    _run("bsa_layer_norm_fwd", _device_of(x, weight, bias, y, mean, rstd), stream,
+         lambda s: load_library().bsa_layer_norm_fwd(ctypes.byref(f), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+                                                     _ptr(mean), _ptr(rstd), s))
+    return y, mean, rstd
+
+
+def layer_norm_workspace_bytes(x: torch.Tensor, weight: torch.Tensor | None = None) -> int:
+    return int(load_library().bsa_layer_norm_workspace_bytes(
+        ctypes.byref(_norm_shape(x, x.dtype, weight, None, 0.0, 0.0))))
+
+
+def alloc_layer_norm_workspace(x: torch.Tensor, weight: torch.Tensor | None = None) -> torch.Tensor:
+    """A workspace of layer_norm_bwd for rows like x's and a weight like this one."""
+    n = layer_norm_workspace_bytes(x, weight)
+    if n == 0:
+        raise ValueError("invalid shape")
+    return torch.empty(n, dtype=torch.uint8, device=x.device)
+
+
+def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                   weight: torch.Tensor | None = None, weight_offset: float = 0.0, want_weight: bool = True,
+                   want_bias: bool = True, dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                   dbias: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor | None]:
+    """Gradients of layer_norm_fwd: dx (x's type), and dweight and dbias in float32, of the
+    weight's shape (None without a weight, or where they are not wanted)."""
+    f = _norm_shape(x, getattr(dy, "dtype", None), weight, None, 0.0, weight_offset)
+    _need(dy, dy.dtype, x.shape, "dy")
+    _need(mean, torch.float32, x.shape[:-1], "mean")
+    _need(rstd, torch.float32, x.shape[:-1], "rstd")
+    if weight is None and (dweight is not None or dbias is not None):
+        raise ValueError("dweight and dbias need the weight")
+    want_weight = weight is not None and (want_weight or dweight is not None)
+    want_bias = weight is not None and (want_bias or dbias is not None)
+    with _owned_by(stream):
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if want_weight and dweight is None:
+            dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
+        if want_bias and dbias is None:
+            dbias = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
+        if ws is None and (want_weight or want_bias):
+            ws = alloc_layer_norm_workspace(x, weight)
+    _need(dx, x.dtype, x.shape, "dx")
+    for name, t in (("dweight", dweight), ("dbias", dbias)):
+        if t is not None:
+            _need(t, torch.float32, weight.shape, name)
+    if ws is not None:
+        _need_ws(ws)
+    _run("bsa_layer_norm_bwd", _device_of(x, dy, mean, rstd, weight, dx, dweight, dbias, ws), stream,
+         lambda s: load_library().bsa_layer_norm_bwd(
+             ctypes.byref(f), _ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx), _ptr(dweight),
+             _ptr(dbias), _ptr(ws), ctypes.c_size_t(0 if ws is None else ws.numel()), s))
+    return dx, dweight, dbias
 
 
 class Buffers:

@@ -72,6 +72,18 @@ bool valid_params(const bsa_geom* g, const bsa_mask_params* p) {
   return true;
 }
 
+bool valid_norm(const bsa_norm_shape* f) {
+  if (!f || f->rows < 1 || f->rows >= (1LL << 40) || f->C < 1 || f->C > 16384) return false;
+  if (f->w_per_item && (f->items < 1 || f->items > 65535 || f->rows % f->items != 0)) return false;
+  for (const int t : {f->x_type, f->y_type, f->w_type})
+    if (t != BSA_BF16 && t != BSA_FP32) return false;
+  return f->eps >= 0.0f && !isinf(f->eps) && isfinite(f->weight_offset);
+}
+
+bool aligned_as(const void* p, int type) {
+  return (reinterpret_cast<uintptr_t>(p) & (type == BSA_BF16 ? 1u : 3u)) == 0;
+}
+
 int device_ok() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
@@ -255,6 +267,39 @@ int bsa_sparse_attn_fwd_fixed_scratch(const bsa_geom* g, const void* qt, const v
                                                     static_cast<const __nv_bfloat16*>(vt), mask, kv_count,
                                                     softmax_scale, static_cast<__nv_bfloat16*>(out), lse,
                                                     kernel_errors, static_cast<cudaStream_t>(stream)));
+}
+
+int bsa_layer_norm_fwd(const bsa_norm_shape* f, const void* x, const void* weight, const void* bias, void* y,
+                       float* mean, float* rstd, void* stream) {
+  const CallRange range("bsa_layer_norm_fwd");
+  if (!valid_norm(f) || !x || !y) return BSA_ERR_INVALID_ARG;
+  if (!aligned_as(x, f->x_type) || !aligned_as(y, f->y_type) || !aligned_as(weight, f->w_type) ||
+      !aligned_as(bias, f->w_type) || !aligned_as(mean, BSA_FP32) || !aligned_as(rstd, BSA_FP32))
+    return BSA_ERR_INVALID_ARG;
+  const int dev = device_ok();
+  if (dev != BSA_OK) return dev;
+  return status_of(launch_norm_fwd(*f, x, weight, bias, y, mean, rstd, static_cast<cudaStream_t>(stream)));
+}
+
+size_t bsa_layer_norm_workspace_bytes(const bsa_norm_shape* f) { return valid_norm(f) ? norm_workspace(*f) : 0; }
+
+int bsa_layer_norm_bwd(const bsa_norm_shape* f, const void* x, const void* dy, const float* mean,
+                       const float* rstd, const void* weight, void* dx, float* dweight, float* dbias, void* ws,
+                       size_t ws_bytes, void* stream) {
+  const CallRange range("bsa_layer_norm_bwd");
+  if (!valid_norm(f) || !x || !dy || !mean || !rstd || !dx) return BSA_ERR_INVALID_ARG;
+  if (!aligned_as(x, f->x_type) || !aligned_as(dy, f->y_type) || !aligned_as(dx, f->x_type) ||
+      !aligned_as(weight, f->w_type) || !aligned_as(mean, BSA_FP32) || !aligned_as(rstd, BSA_FP32) ||
+      !aligned_as(dweight, BSA_FP32) || !aligned_as(dbias, BSA_FP32))
+    return BSA_ERR_INVALID_ARG;
+  if (dweight || dbias) {
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return BSA_ERR_WORKSPACE;
+    if (ws_bytes < norm_workspace(*f)) return BSA_ERR_WORKSPACE;
+  }
+  const int dev = device_ok();
+  if (dev != BSA_OK) return dev;
+  return status_of(launch_norm_bwd(*f, x, dy, mean, rstd, weight, dx, dweight, dbias, ws,
+                                   static_cast<cudaStream_t>(stream)));
 }
 
 uint64_t bsa_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

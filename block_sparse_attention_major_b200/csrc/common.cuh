@@ -145,5 +145,11 @@ cudaError_t launch_sparse_attn_fixed_scratch(const Geom& g, const __nv_bfloat16*
                                              const __nv_bfloat16* vt, const uint32_t* mask,
                                              const int32_t* kv_count, float scale, __nv_bfloat16* out,
                                              float* lse, uint32_t* errors, cudaStream_t s);
+size_t norm_workspace(const bsa_norm_shape& f);
+cudaError_t launch_norm_fwd(const bsa_norm_shape& f, const void* x, const void* w, const void* b, void* y,
+                            float* mean, float* rstd, cudaStream_t s);
+cudaError_t launch_norm_bwd(const bsa_norm_shape& f, const void* x, const void* dy, const float* mean,
+                            const float* rstd, const void* w, void* dx, float* dw, float* db, void* ws,
+                            cudaStream_t s);
 void count_launches(int n);
 }  // namespace bsa

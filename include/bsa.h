@@ -105,6 +105,9 @@ enum {
     BSA_ERR_CUDA = 4                /* a CUDA call or launch failed */
 };
 
+/* Element types of the layer norm's tensors. */
+enum { BSA_BF16 = 0, BSA_FP32 = 1 };
+
 /* Bits of the kernel error word (uint32 at byte 0 of the workspace). */
 enum {
     BSA_KERR_WAIT_TIMEOUT = 1u << 0, /* a bounded barrier wait in a kernel ran out */
@@ -241,6 +244,55 @@ size_t bsa_route_flags_offset(const bsa_geom* g);
 int bsa_sparse_attn_fwd_fixed_scratch(const bsa_geom* g, const void* qt, const void* kt, const void* vt,
                                       const uint32_t* mask, const int32_t* kv_count, float softmax_scale,
                                       void* out, float* lse, uint32_t* kernel_errors, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Layer norm over the last axis. The papers have no counterpart: it is the norm ahead of the
+ * parts of a diffusion transformer's block (with a weight and a bias per batch item, its
+ * modulation), and the per-head norm of Q and K ahead of attention.
+ *   rows, C       the tensor is [rows, C]; 1 <= rows < 2^40, 1 <= C <= 16384
+ *   items         w_per_item: batch items, a divisor of rows, at most 65535; row r belongs to
+ *                 item r / (rows / items). Else ignored
+ *   w_per_item    0: one weight row [C] (and bias row) for every row; 1: one per item, [items, C]
+ *   x_type, y_type, w_type   BSA_BF16 or BSA_FP32: of x and dx; of y and dy; of weight and bias
+ *   eps           added to the variance, >= 0
+ *   weight_offset added to the weight (1 for a modulation stored as the distance from one)
+ * Pointers need the alignment of their element type only; rows whose address and width allow
+ * 16-byte accesses are read faster. */
+typedef struct bsa_norm_shape {
+    long long rows;
+    int C;
+    int items;
+    int w_per_item;
+    int x_type;
+    int y_type;
+    int w_type;
+    float eps;
+    float weight_offset;
+} bsa_norm_shape;
+
+/* y = (x - mean) rstd (weight_offset + weight) + bias, with mean and the biased variance of the
+ * row in fp32, rstd = 1 / sqrt(var + eps).
+ *   x : [rows, C] input;  y : [rows, C] output (may be x itself where the types agree)
+ *   weight, bias : may be NULL (factor 1, whatever weight_offset is; addend 0)
+ *   mean, rstd   : fp32 [rows] outputs for the backward pass; either may be NULL */
+int bsa_layer_norm_fwd(const bsa_norm_shape* f, const void* x, const void* weight, const void* bias, void* y,
+                       float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace of bsa_layer_norm_bwd (needed where dweight or dbias is asked for); 0 for an
+ * invalid shape. Host only. Nothing is kept in it between calls; a call that runs at the same
+ * time needs its own. */
+size_t bsa_layer_norm_workspace_bytes(const bsa_norm_shape* f);
+
+/* Gradients of bsa_layer_norm_fwd from x, dy and the statistics that it wrote.
+ *   dy : [rows, C] (y_type) input;  dx : [rows, C] (x_type) output (may be dy or x itself where
+ *        the types agree)
+ *   dweight, dbias : fp32 outputs of the weight's shape ([C], or [items, C]), sums over the rows
+ *        in fp32 in a fixed order; either may be NULL
+ *   ws : 256-byte aligned; not read when both are NULL
+ * Deterministic: repeated calls give identical bits. */
+int bsa_layer_norm_bwd(const bsa_norm_shape* f, const void* x, const void* dy, const float* mean,
+                       const float* rstd, const void* weight, void* dx, float* dweight, float* dbias, void* ws,
+                       size_t ws_bytes, void* stream);
 
 /* Number of kernels the library launched since it was loaded (all entry points, all
  * threads). Host-side counter, for accounting only. */
