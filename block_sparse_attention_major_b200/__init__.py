@@ -14,6 +14,9 @@ Entry points (same names as the C ABI in include/bsa.h):
     sparse_attn_fwd_token(g, qt, kt, vt, mask, kv_count, dense, token_radius)
                                     the same under a token-level circular support
     forward(g, p, q, k, v, difficulty)       the whole path, raster in, raster out
+    cross_attn_fwd(g, q, k, v, kv_len, key_mask)    attention to an encoder's states of another
+                                    length -> (out bf16 [B,N,H,d], lse fp32 [B,H,N])
+    cross_attn_bwd(g, q, k, v, out, lse, dout, ...)    its gradients -> (dq, dk, dv)
     layer_norm_fwd(x, weight, bias)          -> (y, mean, rstd), over the last axis
     layer_norm_bwd(x, dy, mean, rstd, weight)    -> (dx, dweight, dbias)
 """
@@ -46,6 +49,14 @@ class bsa_mask_params(ctypes.Structure):
     _fields_ = [("window_kind", ctypes.c_int), ("radius", ctypes.c_int), ("topk", ctypes.c_int),
                 ("dense_fraction", ctypes.c_float), ("budget_mode", ctypes.c_int),
                 ("budget_target", ctypes.c_float)]
+
+
+class bsa_cross_geom(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "Hkv", "d", "N", "M")]
+
+
+class bsa_cross_strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_longlong * 3) for n in ("q", "k", "v")]
 
 
 class bsa_norm_shape(ctypes.Structure):
@@ -105,6 +116,13 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.bsa_sparse_attn_fwd_fixed_scratch.restype = ctypes.c_int
         lib.bsa_sparse_attn_fwd_fixed_scratch.argtypes = [G, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp,
                                                           vp, vp]
+        X, T = ctypes.POINTER(bsa_cross_geom), ctypes.POINTER(bsa_cross_strides)
+        lib.bsa_cross_workspace_bytes.restype = sz
+        lib.bsa_cross_workspace_bytes.argtypes = [X]
+        lib.bsa_cross_attn_fwd.restype = ctypes.c_int
+        lib.bsa_cross_attn_fwd.argtypes = [X, T] + [vp] * 5 + [ctypes.c_float] + [vp] * 3 + [sz, vp]
+        lib.bsa_cross_attn_bwd.restype = ctypes.c_int
+        lib.bsa_cross_attn_bwd.argtypes = [X, T] + [vp] * 8 + [ctypes.c_float] + [vp] * 4 + [sz, vp]
         N = ctypes.POINTER(bsa_norm_shape)
         lib.bsa_layer_norm_fwd.restype = ctypes.c_int
         lib.bsa_layer_norm_fwd.argtypes = [N] + [vp] * 7
@@ -149,6 +167,22 @@ class Geometry:
 
     def c(self) -> bsa_geom:
         return bsa_geom(self.B, self.H, self.d, self.T, self.Hs, self.Ws)
+
+
+@dataclass(frozen=True)
+class CrossGeometry:
+    """Shape of an attention call to an encoder's states: B items of N query tokens with H heads,
+    and M encoder states with Hkv key heads (a divisor of H)."""
+
+    B: int
+    H: int
+    Hkv: int
+    d: int
+    N: int
+    M: int
+
+    def c(self) -> bsa_cross_geom:
+        return bsa_cross_geom(self.B, self.H, self.Hkv, self.d, self.N, self.M)
 
 
 @dataclass(frozen=True)
@@ -449,6 +483,108 @@ def sparse_attn_fwd_fixed_scratch(g: Geometry, qt: torch.Tensor, kt: torch.Tenso
              ctypes.byref(g.c()), _ptr(qt), _ptr(kt), _ptr(vt), _ptr(mask), _ptr(kv_count),
              ctypes.c_float(sc), _ptr(out), _ptr(lse), _ptr(kernel_errors), s))
     return out, lse
+
+
+def cross_workspace_bytes(g: CrossGeometry) -> int:
+    return int(load_library().bsa_cross_workspace_bytes(ctypes.byref(g.c())))
+
+
+def alloc_cross_workspace(g: CrossGeometry, device=None) -> torch.Tensor:
+    """A zeroed device workspace of cross_attn_fwd and cross_attn_bwd (byte 0 = kernel error word)."""
+    n = cross_workspace_bytes(g)
+    if n == 0:
+        raise ValueError("invalid geometry")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _need_strided(t: torch.Tensor, shape, name: str) -> None:
+    """A bf16 tensor whose last axis is contiguous; the library checks the other strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last axis")
+
+
+def _cross_inputs(g: CrossGeometry, q, k, v, kv_len, key_mask) -> bsa_cross_strides:
+    _need_strided(q, (g.B, g.N, g.H, g.d), "q")
+    _need_strided(k, (g.B, g.M, g.Hkv, g.d), "k")
+    _need_strided(v, (g.B, g.M, g.Hkv, g.d), "v")
+    if kv_len is not None:
+        _need(kv_len, torch.int32, (g.B,), "kv_len")
+    if key_mask is not None:
+        _need(key_mask, torch.bool, (g.B, g.M), "key_mask")
+    three = ctypes.c_longlong * 3
+    return bsa_cross_strides(*(three(*t.stride()[:3]) for t in (q, k, v)))
+
+
+def cross_attn_fwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   kv_len: torch.Tensor | None = None, key_mask: torch.Tensor | None = None,
+                   scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None, want_lse: bool = True,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Attention of q [B,N,H,d] to the encoder's k, v [B,M,Hkv,d] (bf16; parts of a fused projection
+    may be passed as they are, and k and v expanded over the items).
+
+    kv_len (int32 [B]) and key_mask (bool [B,M]) say which keys of an item are valid; an item
+    without one gives 0 and an lse of -inf. Returns (out bf16 [B,N,H,d], lse fp32 [B,H,N])."""
+    st = _cross_inputs(g, q, k, v, kv_len, key_mask)
+    dev = q.device
+    with _owned_by(stream):
+        if out is None:
+            out = torch.empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16, device=dev)
+        if want_lse and lse is None:
+            lse = torch.empty((g.B, g.H, g.N), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = alloc_cross_workspace(g, dev)
+    _need(out, torch.bfloat16, (g.B, g.N, g.H, g.d), "out")
+    if lse is not None:
+        _need(lse, torch.float32, (g.B, g.H, g.N), "lse")
+    _need_ws(ws)
+    sc = 1.0 / math.sqrt(g.d) if scale is None else float(scale)
+    _run("bsa_cross_attn_fwd", _device_of(q, k, v, kv_len, key_mask, out, lse, ws), stream,
+         lambda s: load_library().bsa_cross_attn_fwd(
+             ctypes.byref(g.c()), ctypes.byref(st), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(key_mask),
+             ctypes.c_float(sc), _ptr(out), _ptr(lse), _ptr(ws), ctypes.c_size_t(ws.numel()), s))
+    return out, lse
+
+
+def cross_attn_bwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                   lse: torch.Tensor, dout: torch.Tensor, kv_len: torch.Tensor | None = None,
+                   key_mask: torch.Tensor | None = None, scale: float | None = None,
+                   dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of cross_attn_fwd from its inputs, its out and lse, and dout: dq [B,N,H,d], and dk
+    and dv [B,M,Hkv,d] per item, zero at keys that are not valid (all bf16)."""
+    st = _cross_inputs(g, q, k, v, kv_len, key_mask)
+    _need(out, torch.bfloat16, (g.B, g.N, g.H, g.d), "out")
+    _need(dout, torch.bfloat16, (g.B, g.N, g.H, g.d), "dout")
+    _need(lse, torch.float32, (g.B, g.H, g.N), "lse")
+    dev = q.device
+    with _owned_by(stream):
+        if dq is None:
+            dq = torch.empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16, device=dev)
+        if dk is None:
+            dk = torch.empty((g.B, g.M, g.Hkv, g.d), dtype=torch.bfloat16, device=dev)
+        if dv is None:
+            dv = torch.empty((g.B, g.M, g.Hkv, g.d), dtype=torch.bfloat16, device=dev)
+        if ws is None:
+            ws = alloc_cross_workspace(g, dev)
+    _need(dq, torch.bfloat16, (g.B, g.N, g.H, g.d), "dq")
+    _need(dk, torch.bfloat16, (g.B, g.M, g.Hkv, g.d), "dk")
+    _need(dv, torch.bfloat16, (g.B, g.M, g.Hkv, g.d), "dv")
+    _need_ws(ws)
+    sc = 1.0 / math.sqrt(g.d) if scale is None else float(scale)
+    _run("bsa_cross_attn_bwd", _device_of(q, k, v, out, lse, dout, kv_len, key_mask, dq, dk, dv, ws), stream,
+         lambda s: load_library().bsa_cross_attn_bwd(
+             ctypes.byref(g.c()), ctypes.byref(st), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+             _ptr(kv_len), _ptr(key_mask), ctypes.c_float(sc), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
+             ctypes.c_size_t(ws.numel()), s))
+    return dq, dk, dv
 
 
 _NORM_TYPES = {torch.bfloat16: 0, torch.float32: 1}

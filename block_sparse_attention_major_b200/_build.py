@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbsa.so")
 OBJDIR = os.path.join(HERE, "_objs")
-SOURCES = ["abi.cu", "reorder.cu", "mask.cu", "score_tc.cu", "attn.cu", "norm.cu", "selftest.cu"]
+SOURCES = ["abi.cu", "reorder.cu", "mask.cu", "score_tc.cu", "attn.cu", "cross_fwd.cu",
+           "cross_bwd.cu", "norm.cu", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

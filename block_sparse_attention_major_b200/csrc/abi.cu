@@ -8,6 +8,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "common.cuh"
+#include "cross.cuh"
 #include "window.cuh"
 
 namespace bsa {
@@ -82,6 +83,53 @@ bool valid_norm(const bsa_norm_shape* f) {
 
 bool aligned_as(const void* p, int type) {
   return (reinterpret_cast<uintptr_t>(p) & (type == BSA_BF16 ? 1u : 3u)) == 0;
+}
+
+bool valid_cross(const bsa_cross_geom* g) {
+  if (!g || g->B < 1 || g->H < 1 || g->Hkv < 1 || g->N < 1 || g->M < 1) return false;
+  if (g->d != 64 && g->d != 128) return false;
+  if (g->H % g->Hkv != 0 || g->H / g->Hkv > kCrossTile) return false;
+  if ((long long)g->B * g->H > 65535) return false;
+  return (long long)g->B * g->H * g->N < (1LL << 31) && (long long)g->B * g->Hkv * g->M < (1LL << 31) - 128;
+}
+
+// Strides of one tensor, dense where st is null; false where they cannot be read by a tensor map.
+bool cross_stride(const long long* st, int items, int tokens, int heads, int d, CrossStride* out) {
+  if (!st) {
+    *out = {(long long)tokens * heads * d, (long long)heads * d, d};
+    return true;
+  }
+  *out = {st[0], st[1], st[2]};
+  const int extent[3] = {items, tokens, heads};
+  for (int i = 0; i < 3; ++i)
+    if (extent[i] > 1 && !(i == 0 && st[i] == 0) && (st[i] < 8 || st[i] % 8 != 0 || st[i] >= (1LL << 38))) return false;
+  return true;
+}
+
+int device_ok();
+
+// The checks shared by both cross-attention calls; fills in what they launch with.
+int check_cross(const bsa_cross_geom* g, const bsa_cross_strides* st, const void* q, const void* k, const void* v,
+                const int32_t* kv_len, const uint8_t* key_mask, float scale, const void* ws, size_t ws_bytes,
+                CrossCall* c) {
+  if (!valid_cross(g) || !aligned16(q) || !aligned16(k) || !aligned16(v)) return BSA_ERR_INVALID_ARG;
+  if (kv_len && (reinterpret_cast<uintptr_t>(kv_len) & 3u) != 0) return BSA_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || isinf(scale)) return BSA_ERR_INVALID_ARG;
+  c->g = make_cross(*g);
+  if (!cross_stride(st ? st->q : nullptr, g->B, g->N, g->H, g->d, &c->sq) ||
+      !cross_stride(st ? st->k : nullptr, g->B, g->M, g->Hkv, g->d, &c->sk) ||
+      !cross_stride(st ? st->v : nullptr, g->B, g->M, g->Hkv, g->d, &c->sv))
+    return BSA_ERR_INVALID_ARG;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return BSA_ERR_WORKSPACE;
+  if (ws_bytes < cross_ws(c->g).total) return BSA_ERR_WORKSPACE;
+  c->q = q;
+  c->k = k;
+  c->v = v;
+  c->kv_len = kv_len;
+  c->key_mask = key_mask;
+  c->scale = scale;
+  c->ws = static_cast<uint8_t*>(const_cast<void*>(ws));
+  return device_ok();
 }
 
 int device_ok() {
@@ -300,6 +348,35 @@ int bsa_layer_norm_bwd(const bsa_norm_shape* f, const void* x, const void* dy, c
   if (dev != BSA_OK) return dev;
   return status_of(launch_norm_bwd(*f, x, dy, mean, rstd, weight, dx, dweight, dbias, ws,
                                    static_cast<cudaStream_t>(stream)));
+}
+
+size_t bsa_cross_workspace_bytes(const bsa_cross_geom* g) {
+  return valid_cross(g) ? cross_ws(make_cross(*g)).total : 0;
+}
+
+int bsa_cross_attn_fwd(const bsa_cross_geom* g, const bsa_cross_strides* st, const void* q, const void* k,
+                       const void* v, const int32_t* kv_len, const uint8_t* key_mask, float softmax_scale,
+                       void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  const CallRange range("bsa_cross_attn_fwd");
+  if (!aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return BSA_ERR_INVALID_ARG;
+  CrossCall c;
+  const int s = check_cross(g, st, q, k, v, kv_len, key_mask, softmax_scale, ws, ws_bytes, &c);
+  if (s != BSA_OK) return s;
+  return status_of(launch_cross_fwd(c, out, lse, static_cast<cudaStream_t>(stream)));
+}
+
+int bsa_cross_attn_bwd(const bsa_cross_geom* g, const bsa_cross_strides* st, const void* q, const void* k,
+                       const void* v, const void* out, const float* lse, const void* dout,
+                       const int32_t* kv_len, const uint8_t* key_mask, float softmax_scale, void* dq, void* dk,
+                       void* dv, void* ws, size_t ws_bytes, void* stream) {
+  const CallRange range("bsa_cross_attn_bwd");
+  if (!aligned16(out) || !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !lse ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return BSA_ERR_INVALID_ARG;
+  CrossCall c;
+  const int s = check_cross(g, st, q, k, v, kv_len, key_mask, softmax_scale, ws, ws_bytes, &c);
+  if (s != BSA_OK) return s;
+  return status_of(launch_cross_bwd(c, out, lse, dout, dq, dk, dv, static_cast<cudaStream_t>(stream)));
 }
 
 uint64_t bsa_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

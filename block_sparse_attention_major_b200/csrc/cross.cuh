@@ -1,0 +1,223 @@
+// Shared parts of the attention of the video tokens to an encoder's states: what a call is,
+// its workspace, and the device helpers of its forward and backward kernels.
+#pragma once
+
+#include "common.cuh"
+#include "sm100_ptx.cuh"
+#include "tmem_ops.cuh"
+
+namespace bsa {
+
+constexpr int kCrossTile = 128;      // query rows and keys of a tile
+constexpr int kCrossSms = 148;       // SMs of the part: bounds persistent grids and their workspace
+
+// One call. The H / Hkv = G query heads of a key head are handled together: a query tile holds
+// tpt = floor(128 / G) tokens, row r = (token r / G, head r % G), so that a key tile is read
+// once for all of them and dk, dv sum over them where they are computed.
+struct CrossGeom {
+  int B, H, Hkv, d, N, M;
+  int G, tpt;                        // query heads of a key head; tokens of a query tile
+  int nqt, nkt;                      // query tiles (of one key head), key tiles
+};
+
+inline CrossGeom make_cross(const bsa_cross_geom& g) {
+  CrossGeom c;
+  c.B = g.B; c.H = g.H; c.Hkv = g.Hkv; c.d = g.d; c.N = g.N; c.M = g.M;
+  c.G = g.H / g.Hkv;
+  c.tpt = kCrossTile / c.G;
+  c.nqt = ceil_div(g.N, c.tpt);
+  c.nkt = ceil_div(g.M, kCrossTile);
+  return c;
+}
+
+// Which keys a batch item attends to: all (both null), the first kv_len[b] (clamped to [0, M]),
+// or, with a mask, the set bits of its packed words; `plan` then holds (last valid key + 1,
+// number of valid keys).
+struct KeySet {
+  const int* kv_len;
+  const int2* plan;
+  const uint32_t* bits;              // [B, 4 nkt]
+};
+
+// Keys that an item reaches (0: none) and the number of valid ones.
+__device__ __forceinline__ int2 item_keys(const KeySet& ks, int b, int M) {
+  if (ks.plan) return ks.plan[b];
+  if (!ks.kv_len) return make_int2(M, M);
+  const int n = min(max(ks.kv_len[b], 0), M);
+  return make_int2(n, n);
+}
+
+// Valid keys of key tile kt as 4 words of 32.
+__device__ __forceinline__ uint4 tile_bits(const KeySet& ks, int b, int kt, int nkt, int len) {
+  if (ks.bits) return reinterpret_cast<const uint4*>(ks.bits)[(long long)b * nkt + kt];
+  const int n = len - kt * kCrossTile;
+  auto word = [&](int i) -> uint32_t {
+    const int m = n - 32 * i;
+    return m >= 32 ? 0xffffffffu : m <= 0 ? 0u : ((1u << m) - 1u);
+  };
+  return make_uint4(word(0), word(1), word(2), word(3));
+}
+__device__ __forceinline__ bool all_set(uint4 w) { return (w.x & w.y & w.z & w.w) == 0xffffffffu; }
+
+// -------------------------------------------------------------------- workspace layout
+// [0, 256)  error word; then, 256-aligned: plan int2 [B], packed key bits u32 [B, 4 nkt], prefix of
+// the items' key tiles int [B + 1], row statistics float2 [B, H, N] (backward), and one region
+// that the forward pass uses for the partial results of split keys, the backward pass for the
+// partial dk, dv of its blocks.
+struct CrossWs {
+  size_t plan, bits, prefix, stats, part, total;
+};
+
+// Parts that the keys are split into when the query tiles alone do not fill the device.
+inline int cross_splits(const CrossGeom& g) {
+  const long long units = (long long)g.B * g.Hkv * ceil_div(g.nqt, 2);
+  if (units * 2 > kCrossSms) return 1;
+  const long long s = kCrossSms / units;
+  return (int)(s < g.nkt ? s : g.nkt);
+}
+
+inline CrossWs cross_ws(const CrossGeom& g) {
+  CrossWs w;
+  size_t off = 256;
+  w.plan = off; off = align256(off + (size_t)g.B * sizeof(int2));
+  w.bits = off; off = align256(off + (size_t)g.B * g.nkt * 16);
+  w.prefix = off; off = align256(off + ((size_t)g.B + 1) * sizeof(int));
+  w.stats = off; off = align256(off + (size_t)g.B * g.H * g.N * sizeof(float2));
+  w.part = off;
+  const int s = cross_splits(g);
+  const size_t fwd = s > 1 ? (size_t)s * g.B * g.N * g.H * (g.d + 1) * sizeof(float) : 0;
+  const size_t bwd = (size_t)kCrossSms * 2 * 2 * kCrossTile * g.d * sizeof(float);
+  w.total = align256(off + (fwd > bwd ? fwd : bwd));
+  return w;
+}
+
+// ------------------------------------------------------------------------ device helpers
+namespace cross {
+
+constexpr long long kWaitLimit = 4000000000LL;     // SM cycles, about 2 s
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Packed pairs of fp32.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void uf2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// All lanes take the same decision after a per-thread bounded wait.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, err, kWaitLimit));
+}
+
+// Box of a 4-D map (columns, heads, tokens, items) into shared memory.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c, int h, int n,
+                                            int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c), "r"(h), "r"(n), "r"(b)
+      : "memory");
+}
+// Orders this thread's shared-memory writes before later reads by the tensor pipe.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Zeroes the rows of masked keys in a [D/64][128 rows][128 B] tile (the whole warp): a row whose
+// probability is zero must not bring an infinity or a NaN into a product over the keys.
+template <int D>
+__device__ __forceinline__ void zero_masked_rows(uint8_t* tile, uint4 w, int lane) {
+  const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    for (uint32_t miss = ~word[i]; miss; miss &= miss - 1) {
+      const int row = 32 * i + __ffs(miss) - 1;
+      if (lane < 8 * (D / 64))
+        *reinterpret_cast<uint4*>(tile + (lane >> 3) * (kCrossTile * 128) + row * 128 + (lane & 7) * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
+  fence_proxy_async();
+  __syncwarp();
+}
+
+// D[128 x 128] = A B^T of two K-major tiles, D/16 steps of 16 columns.
+template <int D>
+__device__ __forceinline__ void product_nt(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem) {
+  constexpr uint32_t id = ptx::idesc_bf16_f32(128, 128, 0, 0);
+  const uint64_t ad = ptx::smem_desc_sw128(a_smem, 16, 1024), bd = ptx::smem_desc_sw128(b_smem, 16, 1024);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t o = (uint64_t)(((kk >> 2) * (kCrossTile * 128) + (kk & 3) * 32) >> 4);
+    ptx::mma_ss(d_tmem, ad + o, bd + o, id, kk > 0 ? 1u : 0u);
+  }
+}
+
+// D[128 x D] (+)= A B of a bf16 A in TMEM (128 contraction columns: 64 32-bit columns, the second
+// half `gap` columns after the first) and a tile B whose rows are the contraction.
+template <int D>
+__device__ __forceinline__ void product_nn(uint32_t d_tmem, uint32_t a_tmem, int gap, uint32_t b_smem, bool accumulate) {
+  constexpr uint32_t id = ptx::idesc_bf16_f32(128, D, 0, 1);
+  const uint64_t bd = ptx::smem_desc_sw128(b_smem, kCrossTile * 128, 1024);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    ptx::mma_ts(d_tmem, a_tmem + (uint32_t)((kk & 3) * 8 + (kk >> 2) * gap), bd + (uint64_t)(kk * (2048 >> 4)), id,
+                (kk > 0 || accumulate) ? 1u : 0u);
+}
+
+}  // namespace cross
+
+// Tensor maps of one call: q-like tensors (boxes of one query tile's tokens and heads) and
+// k-like ones (boxes of 128 keys of one head), 64 columns wide with the 128-byte swizzle.
+struct CrossStride {
+  long long b, n, h;                 // elements
+};
+bool make_map_4d(CUtensorMap* m, const void* base, int d, int heads, int tokens, int items, const CrossStride& s,
+                 int box_heads, int box_tokens);
+
+// Packs a key mask (and kv_len) into `bits` and `plan`.
+cudaError_t launch_pack_keys(const CrossGeom& g, const int* kv_len, const uint8_t* key_mask, int2* plan,
+                             uint32_t* bits, cudaStream_t s);
+
+struct CrossCall {
+  CrossGeom g;
+  CrossStride sq, sk, sv;
+  const void *q, *k, *v;
+  const int* kv_len;
+  const uint8_t* key_mask;
+  float scale;
+  uint8_t* ws;
+};
+cudaError_t launch_cross_fwd(const CrossCall& c, void* out, float* lse, cudaStream_t s);
+cudaError_t launch_cross_bwd(const CrossCall& c, const void* out, const float* lse, const void* dout, void* dq,
+                             void* dk, void* dv, cudaStream_t s);
+
+}  // namespace bsa

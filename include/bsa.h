@@ -294,6 +294,65 @@ int bsa_layer_norm_bwd(const bsa_norm_shape* f, const void* x, const void* dy, c
                        const float* rstd, const void* weight, void* dx, float* dweight, float* dbias, void* ws,
                        size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Attention of the video tokens to an encoder's states of another length (a prompt, an image).
+ * The papers have no counterpart: it is the part of a video diffusion transformer's block that
+ * follows the self-attention, whose sequence of keys is short and padded.
+ *   B, N, M   batch items, query tokens, encoder states (keys) of an item, each >= 1
+ *   H, Hkv    query heads and key heads; Hkv divides H, query head h reads key head
+ *             h / (H / Hkv); H / Hkv <= 128, B*H <= 65535
+ *   d         head dimension, 64 or 128
+ * with B*N*H < 2^31 and B*M*Hkv < 2^31. */
+typedef struct bsa_cross_geom {
+    int B;
+    int H;
+    int Hkv;
+    int d;
+    int N;
+    int M;
+} bsa_cross_geom;
+
+/* Element strides (item, token, head) of q [B, N, H, d] and of k and v [B, M, Hkv, d], whose last
+ * axis is contiguous: for tensors that are parts of a fused projection. Each stride of an axis
+ * of more than one index is a positive multiple of 8, below 2^38; the item stride may be 0 (one
+ * tensor for every item). A NULL pointer to this struct means densely packed. */
+typedef struct bsa_cross_strides {
+    long long q[3];
+    long long k[3];
+    long long v[3];
+} bsa_cross_strides;
+
+/* Bytes of workspace of both calls below (its first 256 bytes hold the error word, which the
+ * caller zeroes once); 0 for an invalid geometry. Host only. Nothing is kept in it between
+ * calls; a call that runs at the same time needs its own. */
+size_t bsa_cross_workspace_bytes(const bsa_cross_geom* g);
+
+/* out = softmax(softmax_scale q k^T) v over the valid keys of each item.
+ *   q, k, v  : bf16, strided as st says
+ *   kv_len   : device int32 [B], or NULL: only the first kv_len[b] keys of item b are valid (values
+ *              outside [0, M] are clamped to it)
+ *   key_mask : device uint8 [B, M], or NULL: only keys with a nonzero byte are valid; with kv_len,
+ *              keys that both allow
+ *   out      : bf16 [B, N, H, d];  lse : fp32 [B, H, N], natural log of the sum of exponentials; may be
+ *              NULL
+ * An item without a valid key gives out = 0 and lse = -inf. What k and v hold at keys that are not
+ * valid does not matter (infinities and NaN included). fp32 scores and statistics, bf16
+ * probabilities into the P.V product, fp32 accumulation. Deterministic. */
+int bsa_cross_attn_fwd(const bsa_cross_geom* g, const bsa_cross_strides* st, const void* q, const void* k,
+                       const void* v, const int32_t* kv_len, const uint8_t* key_mask, float softmax_scale,
+                       void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of bsa_cross_attn_fwd, given its inputs, its out and lse, and the gradient dout of out
+ * (out, dout: bf16 [B, N, H, d]).
+ *   dq     : bf16 [B, N, H, d];  dk, dv : bf16 [B, M, Hkv, d], sums over the query heads of a key
+ *            head, zero at keys that are not valid, and per item also where an item stride is 0
+ * All three are dense. bf16 probabilities and score gradients into the products, fp32
+ * accumulation. Deterministic. */
+int bsa_cross_attn_bwd(const bsa_cross_geom* g, const bsa_cross_strides* st, const void* q, const void* k,
+                       const void* v, const void* out, const float* lse, const void* dout,
+                       const int32_t* kv_len, const uint8_t* key_mask, float softmax_scale, void* dq, void* dk,
+                       void* dv, void* ws, size_t ws_bytes, void* stream);
+
 /* Number of kernels the library launched since it was loaded (all entry points, all
  * threads). Host-side counter, for accounting only. */
 uint64_t bsa_launch_count(void);
