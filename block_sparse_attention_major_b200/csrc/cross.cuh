@@ -149,7 +149,43 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c), "r"(h), "r"(n), "r"(b)
       : "memory");
 }
-// Orders this thread's shared-memory writes before later reads by the tensor pipe.
+// The reverse copy; the part of the box outside the tensor is not written. Completion goes by
+// this thread's bulk groups: `store_read` waits until the shared memory may be written again.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c, int h, int n, int b) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c), "r"(h), "r"(n), "r"(b)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// A barrier of `threads` threads that also tells all of them whether all said yes: after a bounded
+// wait, so that threads whose wait ran out and threads whose did not leave together.
+__device__ __forceinline__ bool bar_all(int id, int threads, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)yes)
+      : "memory");
+  return r != 0;
+}
+
+// 32 columns of a row (16 bf16 pairs) into columns 32 ch .. of a [D/64][128 rows][128 B] tile with
+// the 128-byte swizzle (16-byte piece i of row r at i xor (r mod 8)).
+__device__ __forceinline__ void put_row32(uint8_t* tile, int row, int ch, const uint32_t (&pk)[16]) {
+  uint8_t* p = tile + (ch >> 1) * (kCrossTile * 128) + row * 128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(p + ((((ch & 1) * 4 + i) ^ (row & 7)) << 4)) =
+        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+}
+
+// Orders this thread's shared-memory writes before later reads by the tensor pipe and the copies.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Zeroes the rows of masked keys in a [D/64][128 rows][128 B] tile (the whole warp): a row whose

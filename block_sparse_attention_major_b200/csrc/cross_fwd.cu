@@ -15,11 +15,15 @@
 // two operands of a 128 x 64 x 16 step are read in 48 cycles and multiplied in 32; of a
 // 128 x 128 x 16 step, 64 and 64).
 //
-// CTA roles (384 threads): warps 0-3 and 4-7 are the softmax of blocks A and B, a row (TMEM lane)
-// a thread; lane 0 of warp 8 loads Q and the K ring; warp 10 loads the V ring and zeroes rows of
-// masked keys; lane 0 of warps 9 and 11 issues the products of A and of B. A block's scores are
-// 128 TMEM columns, P overwrites them as bf16 pairs, and the block's next scores follow its P V
-// in the pipe's issue order, so that one block multiplies while the other exponentiates.
+// CTA roles (512 threads): warps 0-3 and 4-7 are the softmax of blocks A and B, a row (TMEM lane)
+// a thread; warps 8-11 write the finished blocks out (normalise, stage in shared memory, one
+// copy of the whole block); lane 0 of warp 12 loads Q and the K ring; warp 13 loads the V ring
+// and zeroes rows of masked keys; lane 0 of warp 14 issues all products. A block's scores are 128
+// TMEM columns, P overwrites them as bf16 pairs, and the block's next scores follow its P V in the
+// pipe's issue order. One thread issues for A and B in turn: that keeps the blocks half a period
+// apart, so that one multiplies while the other exponentiates (with an issuer for each, their
+// products interleaved in the pipe, both softmaxes waited and then shared the exponential unit:
+// 4200 cycles for a key tile of both blocks, the sum of the two parts).
 //
 // Roundings to fewer bits: P to bf16 for the P V product, the output once. The sum of a row is
 // that of the unrounded probabilities.
@@ -32,11 +36,13 @@ namespace {
 
 using namespace cross;
 
-constexpr int kThreads = 384;
-constexpr int kRegsLaunch = 168;
-constexpr int kRegsSoftmax = 200;
-constexpr int kRegsControl = 104;
-static_assert(128 * (2 * kRegsSoftmax + kRegsControl) <= kThreads * kRegsLaunch, "register split above the launch's pool");
+constexpr int kThreads = 512;
+constexpr int kRegsLaunch = 128;
+constexpr int kRegsSoftmax = 184;
+constexpr int kRegsOut = 80;
+constexpr int kRegsControl = 64;
+static_assert(128 * (2 * kRegsSoftmax + kRegsOut + kRegsControl) <= kThreads * kRegsLaunch,
+              "register split above the launch's pool");
 constexpr float kRescaleLog2 = 8.0f;     // O is rescaled only past 2^8 of growth
 
 template <int D>
@@ -46,9 +52,12 @@ struct Cfg {
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kTile;
   static constexpr int kV = kK + kStages * kTile;
-  static constexpr int kBar = kV + kStages * kTile;
-  // kfull, kempty, vfull, vempty, vland [kStages each]; qfull, qempty, sfull, pfull, odone, drain [2 each]
-  static constexpr int kBars = 5 * kStages + 12;
+  static constexpr int kOut = kV + kStages * kTile;       // staging of one finished block
+  static constexpr int kInv = kOut + kTile;               // [2][128] 1 / row sum
+  static constexpr int kBar = kInv + 2 * kCrossTile * 4;
+  // kfull, kempty, vfull, vempty, vland [kStages each]; qfull, qempty, sfull, pfull, odone, lfull, oempty [2 each],
+  // drain
+  static constexpr int kBars = 5 * kStages + 15;
   static constexpr int kMisc = kBar + 8 * kBars;          // TMEM base, abort
   static constexpr int kSmem = 1024 + kMisc + 16;
   static_assert(kSmem <= 232448, "shared memory");
@@ -68,7 +77,9 @@ struct Bars {
   __device__ uint32_t sfull(int x) const { return b0 + 8 * (5 * S + 4 + x); }
   __device__ uint32_t pfull(int x) const { return b0 + 8 * (5 * S + 6 + x); }
   __device__ uint32_t odone(int x) const { return b0 + 8 * (5 * S + 8 + x); }
-  __device__ uint32_t drain(int x) const { return b0 + 8 * (5 * S + 10 + x); }
+  __device__ uint32_t lfull(int x) const { return b0 + 8 * (5 * S + 10 + x); }
+  __device__ uint32_t oempty(int x) const { return b0 + 8 * (5 * S + 12 + x); }
+  __device__ uint32_t drain() const { return b0 + 8 * (5 * S + 14); }
 };
 
 struct FwdArgs {
@@ -101,21 +112,21 @@ struct Unit {
   }
 };
 
-// Row maximum over 32 columns, of the slots in `w` if masked.
+// Row maximum over 32 columns, of the slots in `w` if masked, in four chains.
 template <bool kMasked>
-__device__ __forceinline__ float max32(const uint32_t* r, uint32_t w, float m) {
-  float a0 = m, a1 = -INFINITY;
+__device__ __forceinline__ void max32(const uint32_t* r, uint32_t w, float (&m)[4]) {
 #pragma unroll
-  for (int c = 0; c < 32; c += 4) {
-    if (kMasked) {
+  for (int c = 0; c < 32; c += 8) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a0 = fmaxf(a0, ((w >> (c + j)) & 1u) ? __uint_as_float(r[c + j]) : -INFINITY);
-    } else {
-      a0 = max3(a0, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-      a1 = max3(a1, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+    for (int j = 0; j < 4; ++j) {
+      float u = __uint_as_float(r[c + 2 * j]), v = __uint_as_float(r[c + 2 * j + 1]);
+      if (kMasked) {
+        u = ((w >> (c + 2 * j)) & 1u) ? u : -INFINITY;
+        v = ((w >> (c + 2 * j + 1)) & 1u) ? v : -INFINITY;
+      }
+      m[j] = max3(m[j], u, v);
     }
   }
-  return fmaxf(a0, a1);
 }
 
 // p = 2^(c s - m) of 32 columns, stored as 16 columns of bf16 pairs; their fp32 sum joins `sum`.
@@ -138,10 +149,36 @@ __device__ __forceinline__ void exp32(const uint32_t* r, uint32_t w, float c, fl
   tmem_st_x16(taddr, pk);
 }
 
+// A key tile in the order in which the issuer meets them: the tiles of a unit, then the next unit
+// with any. `rows[x]` counts the units of block x so far, empty ones included.
+struct TileCursor {
+  int u, kt, t0, t1;
+  bool valid, has_b;
+  uint32_t rows[2];
+  __device__ __forceinline__ void open(const FwdArgs& a, int from) {
+    for (u = from; u < a.units; u += gridDim.x) {
+      const Unit t(a, u);
+      has_b = t.n0 + a.g.tpt < a.g.N;
+      ++rows[0];
+      rows[1] += has_b;
+      t0 = kt = t.t0;
+      t1 = t.t1;
+      if (t0 < t1) {
+        valid = true;
+        return;
+      }
+    }
+    valid = false;
+  }
+  __device__ __forceinline__ void next(const FwdArgs& a) {
+    if (++kt == t1) open(a, u + (int)gridDim.x);
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const FwdArgs a) {
   using C = Cfg<D>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -152,13 +189,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Bars<D> bar{sbase + C::kBar};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
+  float* s_inv = reinterpret_cast<float*>(smem + C::kInv);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       ptx::mbar_init(bar.kfull(s), 1);
-      ptx::mbar_init(bar.kempty(s), 2);       // one release per issuer
+      ptx::mbar_init(bar.kempty(s), 1);
       ptx::mbar_init(bar.vfull(s), 1);
-      ptx::mbar_init(bar.vempty(s), 2);
+      ptx::mbar_init(bar.vempty(s), 1);
       ptx::mbar_init(bar.vland(s), 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -167,23 +205,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar.sfull(x), 1);
       ptx::mbar_init(bar.pfull(x), 4);        // one arrival per softmax warp
       ptx::mbar_init(bar.odone(x), 1);
-      ptx::mbar_init(bar.drain(x), 1);
+      ptx::mbar_init(bar.lfull(x), 4);
+      ptx::mbar_init(bar.oempty(x), 4);       // one per output warp
     }
+    ptx::mbar_init(bar.drain(), 1);
     *abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 14) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *tmem_slot;           // S_A at 0, S_B at 128, O_A at 256, O_B at 256 + D
 
-  if (warp >= 8) {
+  if (warp >= 12) {
     ptx::setmaxnreg_dec<kRegsControl>();
-    if (warp == 8) {
+    if (warp == 12) {
       // ------------------------------------------------------------- Q and the K ring
       if (lane == 0) {
         ptx::prefetch_tensormap(&tmQ);
@@ -226,10 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 2; ++x)
           if (nq[x] > 0) ptx::mbar_wait(bar.qfull(x), (nq[x] - 1) & 1, &zero, a.err, kWaitLimit);
       }
-    } else if (warp == 10) {
+    } else if (warp == 13) {
       // ------------------------------------------------------------- the V ring
       // A tile with masked keys lands on a barrier of its own; its masked rows are zeroed before
-      // the issuers see it (zero probability times an infinity would be a NaN).
+      // the issuer sees it (zero probability times an infinity would be a NaN).
       uint32_t nv = 0, land[S];
 #pragma unroll
       for (int s = 0; s < S; ++s) land[s] = 0;
@@ -269,70 +309,132 @@ __global__ void __launch_bounds__(kThreads, 1)
       int zero = 0;
       for (uint32_t s = 0; s < S; ++s)
         if (nv > s) ptx::mbar_wait(bar.vfull((int)s), ((nv - 1 - s) / S) & 1, &zero, a.err, kWaitLimit);
-    } else {
-      // ------------------------------------------------------------- MMA issuers
-      const int x = warp == 9 ? 0 : 1;
+    } else if (warp == 14) {
+      // ------------------------------------------------------------- MMA issuer
+      // For each key tile, A and then B: P V of this tile, then the scores of the next (which
+      // may be the next unit's first).
       if (lane == 0) {
-        uint32_t nk = 0, nv = 0, np = 0, nq = 0;
-        const uint32_t s_tmem = tmem + 128u * (uint32_t)x, o_tmem = tmem + 256u + (uint32_t)(x * D);
-        const uint32_t q_smem = sbase + C::kQ + x * C::kTile;
+        uint32_t nk = 0, nv = 0, np[2] = {0, 0}, nq[2] = {0, 0};
         auto wait = [&](uint32_t b, uint32_t ph) { return ptx::mbar_wait(b, ph, abort, a.err, kWaitLimit); };
-        bool ok = true;
-        for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-          const Unit t(a, u);
-          const int nt = t.t1 - t.t0;
-          if (nt == 0) continue;
-          const bool has = t.n0 + x * g.tpt < g.N;
-          if (has && !wait(bar.qfull(x), nq & 1)) break;
-          // Scores of key tile i; position i of the K ring is passed either way.
-          auto scores = [&](int i) {
-            const int s = (int)(nk % S);
-            if (!wait(bar.kfull(s), (nk / S) & 1)) return false;
-            ++nk;
-            if (!has) {
-              ptx::mbar_arrive(bar.kempty(s));
-              return true;
-            }
-            ptx::tc_fence_after();
-            product_nt<D>(s_tmem, q_smem, sbase + C::kK + s * C::kTile);
-            ptx::mma_commit(bar.sfull(x));
+        TileCursor cur, nxt;
+        nxt.rows[0] = nxt.rows[1] = 0;
+        nxt.open(a, blockIdx.x);
+        auto scores = [&](int x) {
+          const int s = (int)(nk % S);
+          if (nxt.kt == nxt.t0 && !wait(bar.qfull(x), nq[x]++ & 1)) return false;
+          if (!wait(bar.kfull(s), (nk / S) & 1)) return false;
+          ptx::tc_fence_after();
+          product_nt<D>(tmem + 128u * (uint32_t)x, sbase + C::kQ + x * C::kTile, sbase + C::kK + s * C::kTile);
+          ptx::mma_commit(bar.sfull(x));
+          if (nxt.kt == nxt.t1 - 1) ptx::mma_commit(bar.qempty(x));
+          if (x == 1 || !nxt.has_b) {
             ptx::mma_commit(bar.kempty(s));
-            if (i == nt - 1) ptx::mma_commit(bar.qempty(x));
-            return true;
-          };
-          if (!scores(0)) break;
-          for (int i = 0; i < nt; ++i) {
-            const int s = (int)(nv % S);
-            if (!wait(bar.vfull(s), (nv / S) & 1)) { ok = false; break; }
-            ++nv;
-            if (!has) {
-              ptx::mbar_arrive(bar.vempty(s));
-            } else {
-              if (!wait(bar.pfull(x), np++ & 1)) { ok = false; break; }
-              ptx::tc_fence_after();
-              product_nn<D>(o_tmem, s_tmem, 32, sbase + C::kV + s * C::kTile, i > 0);
-              ptx::mma_commit(bar.vempty(s));
-              if (i == nt - 1) ptx::mma_commit(bar.odone(x));
-            }
-            if (i + 1 < nt && !scores(i + 1)) { ok = false; break; }
+            ++nk;
           }
-          if (has) ++nq;
+          return true;
+        };
+        bool ok = !nxt.valid || (scores(0) && (!nxt.has_b || scores(1)));
+        while (ok && nxt.valid) {
+          cur = nxt;
+          nxt.next(a);
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (x == 0 || cur.has_b) {
+              const int s = (int)(nv % S);
+              // the unit before must have been read out of O
+              if (cur.kt == cur.t0 && cur.rows[x] > 1 && !wait(bar.oempty(x), cur.rows[x] & 1)) { ok = false; break; }
+              if (!wait(bar.vfull(s), (nv / S) & 1) || !wait(bar.pfull(x), np[x]++ & 1)) { ok = false; break; }
+              ptx::tc_fence_after();
+              product_nn<D>(tmem + 256u + (uint32_t)(x * D), tmem + 128u * (uint32_t)x, 32, sbase + C::kV + s * C::kTile,
+                            cur.kt > cur.t0);
+              if (cur.kt == cur.t1 - 1) ptx::mma_commit(bar.odone(x));
+              if (x == 1 || !cur.has_b) {
+                ptx::mma_commit(bar.vempty(s));
+                ++nv;
+              }
+            }
+            if (nxt.valid && (x == 0 || nxt.has_b)) ok = scores(x);
+          }
         }
         // Never free TMEM under a running product.
         int zero = 0;
-        ptx::mma_commit(bar.drain(x));
-        ptx::mbar_wait(bar.drain(x), 0, &zero, a.err, kWaitLimit);
+        ptx::mma_commit(bar.drain());
+        ptx::mbar_wait(bar.drain(), 0, &zero, a.err, kWaitLimit);
       }
     }
+  } else if (warp >= 8) {
+    // --------------------------------------------------------------- output
+    ptx::setmaxnreg_dec<kRegsOut>();
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    uint8_t* stage = smem + C::kOut;
+    uint32_t nl[2] = {0, 0}, no[2] = {0, 0};
+    bool ok = true;
+    for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+      const Unit t(a, u);
+      const bool any = t.t1 > t.t0;
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        const int first = t.n0 + x * g.tpt;
+        if (first >= g.N) continue;
+        ok = warp_wait(bar.lfull(x), nl[x]++ & 1, abort, a.err) &&
+             (!any || warp_wait(bar.odone(x), no[x]++ & 1, abort, a.err));
+        if (threadIdx.x == 256) store_read();                 // the staging is free again
+        ok = bar_all(1, 128, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const float inv = s_inv[x * kCrossTile + row];
+        const uint32_t o_tmem = tmem + 256u + (uint32_t)(x * D) + lane_base;
+        const int tok = first + row / g.G, head = t.hkv * g.G + row % g.G;
+        const bool mine = row < g.G * g.tpt && tok < g.N;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          if (any) {
+            tmem_ld_x32(o_tmem + 32 * ch, o);
+            ptx::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
+          if (a.splits == 1) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) pk[k] = pack_bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+            put_row32(stage, row, ch, pk);
+          } else if (mine) {
+            uint4* dst = reinterpret_cast<uint4*>(
+                a.part_o + ((((long long)t.part * g.B + t.b) * g.N + tok) * g.H + head) * D + 32 * ch);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar.oempty(x));
+        if (a.splits == 1) {
+          fence_proxy_async();
+          bar_sync(1, 128);
+          if (threadIdx.x == 256) {
+#pragma unroll
+            for (int cb = 0; cb < D / 64; ++cb)
+              tma_store_4d(&tmO, sbase + C::kOut + cb * (kCrossTile * 128), cb * 64, t.hkv * g.G, first, t.b);
+            store_commit();
+          }
+        }
+      }
+    }
+    if (threadIdx.x == 256) store_done();
   } else {
-    // --------------------------------------------------------------- softmax + epilogue
+    // --------------------------------------------------------------- softmax
     ptx::setmaxnreg_inc<kRegsSoftmax>();
     const int x = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + 128u * (uint32_t)x + lane_base;
     const uint32_t o_tmem = tmem + 256u + (uint32_t)(x * D) + lane_base;
     const float c = a.scale_log2;
-    uint32_t ns = 0, no = 0;
+    uint32_t ns = 0, nu = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
       const Unit t(a, u);
@@ -348,17 +450,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 4; ++h) tmem_ld_x32(s_tmem + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * h]));
         ptx::tmem_wait_ld();
         const bool full = all_set(w);
-        float mx = -INFINITY;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if (full) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) mx = max32<false>(&r[32 * h], 0u, mx);
+          for (int h = 0; h < 4; ++h) max32<false>(&r[32 * h], 0u, mx);
         } else {
-          mx = max32<true>(&r[0], w.x, mx);
-          mx = max32<true>(&r[32], w.y, mx);
-          mx = max32<true>(&r[64], w.z, mx);
-          mx = max32<true>(&r[96], w.w, mx);
+          max32<true>(&r[0], w.x, mx);
+          max32<true>(&r[32], w.y, mx);
+          max32<true>(&r[64], w.z, mx);
+          max32<true>(&r[96], w.w, mx);
         }
-        const float mb = mx * c;
+        const float mb = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
         bool resc = false;
         if (m_run == -INFINITY) m_run = mb;            // nothing of this row is in O yet but zeros
         else resc = mb > m_run + kRescaleLog2;
@@ -366,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // These scores follow the previous tile's P V in the pipe, so O holds exactly the
           // tiles before this one.
           const float alpha = resc ? ex2(m_run - mb) : 1.0f;
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < D / 16; ++h) {
             uint32_t o[16];
             tmem_ld_x16(o_tmem + 16 * h, o);
@@ -398,59 +500,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bar.pfull(x));
       }
       if (!ok) break;
-      const bool any = t.t1 > t.t0;
-      if (any) {
-        if (!warp_wait(bar.odone(x), no++ & 1, abort, a.err)) break;
-        ptx::tc_fence_after();
-      }
+      // 1 / l for the output warps, once they have read the unit before; the lse from here
+      if (nu > 0 && !warp_wait(bar.oempty(x), (nu - 1) & 1, abort, a.err)) break;
+      ++nu;
+      s_inv[x * kCrossTile + row] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : NAN);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar.lfull(x));
       const int tok = first + row / g.G, head = t.hkv * g.G + row % g.G;
-      const bool mine = row < g.G * g.tpt && tok < g.N;
-      const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : NAN);
-      const float lse2 = l > 0.f ? (m_run == -INFINITY ? 0.0f : m_run) + __log2f(l) : (l == 0.f ? -INFINITY : NAN);
-      const long long at = ((long long)t.b * g.N + tok) * g.H + head;
-      const long long at_lse = ((long long)t.b * g.H + head) * g.N + tok;
-      // The next unit's first P V overwrites O: it follows that unit's first P, which this warp
-      // releases after the reads below.
-#pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t o[32];
-        if (any) {
-          tmem_ld_x32(o_tmem + 32 * ch, o);
-          ptx::tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
-        }
-        if (!mine) continue;
-        if (a.splits > 1) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + ((long long)t.part * g.B * g.N * g.H + at) * D + 32 * ch);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                                 __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * ch);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 v;
-            v.x = pack_bf16x2(__uint_as_float(o[8 * k + 0]) * inv, __uint_as_float(o[8 * k + 1]) * inv);
-            v.y = pack_bf16x2(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv);
-            v.z = pack_bf16x2(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv);
-            v.w = pack_bf16x2(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv);
-            dst[k] = v;
-          }
-        }
-      }
-      if (mine) {
-        if (a.splits > 1) a.part_lse[(long long)t.part * g.B * g.H * g.N + at_lse] = lse2;
-        else if (a.lse) a.lse[at_lse] = lse2 * 0.69314718055994531f;
+      if (row < g.G * g.tpt && tok < g.N) {
+        const float lse2 = l > 0.f ? (m_run == -INFINITY ? 0.0f : m_run) + __log2f(l) : (l == 0.f ? -INFINITY : NAN);
+        const long long at = ((long long)t.b * g.H + head) * g.N + tok;
+        if (a.splits > 1) a.part_lse[(long long)t.part * g.B * g.H * g.N + at] = lse2;
+        else if (a.lse) a.lse[at] = lse2 * 0.69314718055994531f;
       }
     }
   }
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 14) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
@@ -540,16 +608,16 @@ EncodeTiledFn encode_fn() {
 }
 
 template <int D>
-cudaError_t run_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const FwdArgs& a,
-                    cudaStream_t s) {
+cudaError_t run_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
+                    const FwdArgs& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
   // A register split above what the launch provides would wait forever in setmaxnreg.
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, cross_fwd_kernel<D>);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs * kThreads < 128 * (2 * kRegsSoftmax + kRegsControl)) return cudaErrorInvalidConfiguration;
-  cross_fwd_kernel<D><<<a.units < kCrossSms ? a.units : kCrossSms, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, a);
+  if (fa.numRegs * kThreads < 128 * (2 * kRegsSoftmax + kRegsOut + kRegsControl)) return cudaErrorInvalidConfiguration;
+  cross_fwd_kernel<D><<<a.units < kCrossSms ? a.units : kCrossSms, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, mo, a);
   count_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
@@ -611,12 +679,14 @@ cudaError_t launch_cross_fwd(const CrossCall& c, void* out, float* lse, cudaStre
   a.part_lse = a.part_o + (size_t)a.splits * g.B * g.N * g.H * g.d;
   a.err = reinterpret_cast<uint32_t*>(c.ws);
   a.scale_log2 = c.scale * 1.4426950408889634f;
-  CUtensorMap mq, mk, mv;
+  const CrossStride dense = {(long long)g.N * g.H * g.d, (long long)g.H * g.d, g.d};
+  CUtensorMap mq, mk, mv, mo;
   if (!make_map_4d(&mq, c.q, g.d, g.H, g.N, g.B, c.sq, g.G, g.tpt) ||
       !make_map_4d(&mk, c.k, g.d, g.Hkv, g.M, g.B, c.sk, 1, kCrossTile) ||
-      !make_map_4d(&mv, c.v, g.d, g.Hkv, g.M, g.B, c.sv, 1, kCrossTile))
+      !make_map_4d(&mv, c.v, g.d, g.Hkv, g.M, g.B, c.sv, 1, kCrossTile) ||
+      !make_map_4d(&mo, out, g.d, g.H, g.N, g.B, dense, g.G, g.tpt))
     return cudaErrorInvalidValue;
-  return g.d == 128 ? run_fwd<128>(mq, mk, mv, a, s) : run_fwd<64>(mq, mk, mv, a, s);
+  return g.d == 128 ? run_fwd<128>(mq, mk, mv, mo, a, s) : run_fwd<64>(mq, mk, mv, mo, a, s);
 }
 
 }  // namespace bsa
