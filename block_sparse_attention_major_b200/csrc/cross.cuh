@@ -205,6 +205,17 @@ __device__ __forceinline__ void zero_masked_rows(uint8_t* tile, uint4 w, int lan
   __syncwarp();
 }
 
+// One lane of a converged warp, always the same one. The issuing warps run whole, and only the
+// products and commits themselves are left to this lane: their descriptors are then values of the
+// warp, which the tensor instructions take as they are. (Issued from a loop of one lane, each
+// product's operands were moved over one by one, between the softmax warps' instructions: 120
+// cycles a step of 64.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // D[128 x 128] = A B^T of two K-major tiles, D/16 steps of 16 columns.
 template <int D>
 __device__ __forceinline__ void product_nt(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem) {
@@ -219,14 +230,19 @@ __device__ __forceinline__ void product_nt(uint32_t d_tmem, uint32_t a_smem, uin
 
 // D[128 x D] (+)= A B of a bf16 A in TMEM (128 contraction columns: 64 32-bit columns, the second
 // half `gap` columns after the first) and a tile B whose rows are the contraction.
-template <int D>
-__device__ __forceinline__ void product_nn(uint32_t d_tmem, uint32_t a_tmem, int gap, uint32_t b_smem, bool accumulate) {
+template <int D, int kHalf>
+__device__ __forceinline__ void product_nn_half(uint32_t d_tmem, uint32_t a_tmem, int gap, uint32_t b_smem, bool accumulate) {
   constexpr uint32_t id = ptx::idesc_bf16_f32(128, D, 0, 1);
   const uint64_t bd = ptx::smem_desc_sw128(b_smem, kCrossTile * 128, 1024);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    ptx::mma_ts(d_tmem, a_tmem + (uint32_t)((kk & 3) * 8 + (kk >> 2) * gap), bd + (uint64_t)(kk * (2048 >> 4)), id,
-                (kk > 0 || accumulate) ? 1u : 0u);
+  for (int k = 0; k < 4; ++k)
+    ptx::mma_ts(d_tmem, a_tmem + (uint32_t)(k * 8 + kHalf * gap), bd + (uint64_t)((4 * kHalf + k) * (2048 >> 4)), id,
+                (k > 0 || kHalf || accumulate) ? 1u : 0u);
+}
+template <int D>
+__device__ __forceinline__ void product_nn(uint32_t d_tmem, uint32_t a_tmem, int gap, uint32_t b_smem, bool accumulate) {
+  product_nn_half<D, 0>(d_tmem, a_tmem, gap, b_smem, accumulate);
+  product_nn_half<D, 1>(d_tmem, a_tmem, gap, b_smem, true);
 }
 
 }  // namespace cross

@@ -212,55 +212,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9) {
     // ------------------------------------------------------------- MMA issuer
     // S(0), T(0); then for each tile: S of the next one (its buffer's dS went into the product two
-    // back, issued before), dq += dS K, T of the next one (T was read when dS was written).
-    if (lane == 0) {
-      uint32_t ns = 0, nk = 0, nv = 0, nds = 0, nq = 0;
-      bool ok = true;
-      auto scores = [&](bool last) {
-        const int s = (int)(ns % KS);
-        if (!wait(kfull(s), (ns / KS) & 1)) return false;
-        ptx::tc_fence_after();
+    // back, issued before), dq += dS K, T of the next one (T was read when dS was written). The
+    // warp runs whole; one lane issues.
+    uint32_t ns = 0, nk = 0, nv = 0, nds = 0, nq = 0;
+    bool ok = true;
+    auto all_wait = [&](uint32_t b, uint32_t ph) { return warp_wait(b, ph, abort, a.err); };
+    auto scores = [&](bool last) {
+      const int s = (int)(ns % KS);
+      if (!all_wait(kfull(s), (ns / KS) & 1)) return false;
+      ptx::tc_fence_after();
+      if (elect_one()) {
         product_nt<D>(tmem + 128u * (ns & 1), sbase + C::kQ, sbase + C::kK + s * C::kTile);
         ptx::mma_commit(sfull((int)(ns & 1)));
         if (last) ptx::mma_commit(qempty);
-        ++ns;
-        return true;
-      };
-      auto tee = [&](bool last) {
-        const int s = (int)(nv % VS);
-        if (!wait(vfull(s), (nv / VS) & 1)) return false;
-        ptx::tc_fence_after();
+      }
+      __syncwarp();
+      ++ns;
+      return true;
+    };
+    auto tee = [&](bool last) {
+      const int s = (int)(nv % VS);
+      if (!all_wait(vfull(s), (nv / VS) & 1)) return false;
+      ptx::tc_fence_after();
+      if (elect_one()) {
         product_nt<D>(tmem + 256u, sbase + C::kDo, sbase + C::kV + s * C::kTile);
         ptx::mma_commit(tfull);
         ptx::mma_commit(vempty(s));
         if (last) ptx::mma_commit(doempty);
-        ++nv;
-        return true;
-      };
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        int qt, hkv, b;
-        decode(u, qt, hkv, b);
-        const int nt = key_tiles(a, b);
-        if (nt == 0) continue;
-        if (!wait(qfull, nq & 1) || !scores(nt == 1)) break;
-        if (!wait(dofull, nq & 1) || !tee(nt == 1)) break;
-        ++nq;
-        for (int i = 0; i < nt; ++i) {
-          if (i + 1 < nt && !scores(i + 2 == nt)) { ok = false; break; }
-          if (!wait(dsfull, nds++ & 1)) { ok = false; break; }
-          ptx::tc_fence_after();
-          const int s = (int)(nk % KS);
+      }
+      __syncwarp();
+      ++nv;
+      return true;
+    };
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      int qt, hkv, b;
+      decode(u, qt, hkv, b);
+      const int nt = key_tiles(a, b);
+      if (nt == 0) continue;
+      if (!all_wait(qfull, nq & 1) || !scores(nt == 1)) break;
+      if (!all_wait(dofull, nq & 1) || !tee(nt == 1)) break;
+      ++nq;
+      for (int i = 0; i < nt; ++i) {
+        if (i + 1 < nt && !scores(i + 2 == nt)) { ok = false; break; }
+        if (!all_wait(dsfull, nds++ & 1)) { ok = false; break; }
+        ptx::tc_fence_after();
+        const int s = (int)(nk % KS);
+        if (elect_one()) {
           product_nn<D>(tmem + 384u, tmem + 128u * (nk & 1), 64, sbase + C::kK + s * C::kTile, i > 0);
           ptx::mma_commit(kempty(s));
           if (i == nt - 1) ptx::mma_commit(done);
-          ++nk;
-          if (i + 1 < nt && !tee(i + 2 == nt)) { ok = false; break; }
         }
+        __syncwarp();
+        ++nk;
+        if (i + 1 < nt && !tee(i + 2 == nt)) { ok = false; break; }
       }
-      int zero = 0;                                 // never free TMEM under a running product
-      ptx::mma_commit(drain);
-      ptx::mbar_wait(drain, 0, &zero, a.err, kWaitLimit);
     }
+    int zero = 0;                                   // never free TMEM under a running product
+    if (elect_one()) ptx::mma_commit(drain);
+    ptx::mbar_wait(drain, 0, &zero, a.err, kWaitLimit);
   } else if (warp < 8) {
     // ------------------------------------------------------------- dS and the epilogue
     const int half = warp >> 2, row = threadIdx.x & 127;
@@ -546,56 +555,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9) {
     // ------------------------------------------------------------- MMA issuer
     // S(0), T(0); then for each query tile: dv += P dO, S of the next tile (over P, which that
-    // product has read), dk += dS Q, T of the next tile (over dS).
-    if (lane == 0) {
-      uint32_t nseg = 0, ns = 0, nt = 0, n = 0;
-      bool ok = true;
-      auto scores = [&]() {
-        const int s = (int)(ns % S);
-        if (!wait(qfull(s), (ns / S) & 1)) return false;
-        ptx::tc_fence_after();
+    // product has read), dk += dS Q, T of the next tile (over dS). The warp runs whole; one lane
+    // issues.
+    uint32_t nseg = 0, ns = 0, nt = 0, n = 0;
+    bool ok = true;
+    auto all_wait = [&](uint32_t b, uint32_t ph) { return warp_wait(b, ph, abort, a.err); };
+    auto scores = [&]() {
+      const int s = (int)(ns % S);
+      if (!all_wait(qfull(s), (ns / S) & 1)) return false;
+      ptx::tc_fence_after();
+      if (elect_one()) {
         product_nt<D>(tmem, sbase + C::kK, sbase + C::kQ + s * C::kTile);
         ptx::mma_commit(sfull);
-        ++ns;
-        return true;
-      };
-      auto tee = [&]() {
-        const int s = (int)(nt % S);
-        if (!wait(dofull(s), (nt / S) & 1)) return false;
-        ptx::tc_fence_after();
+      }
+      __syncwarp();
+      ++ns;
+      return true;
+    };
+    auto tee = [&]() {
+      const int s = (int)(nt % S);
+      if (!all_wait(dofull(s), (nt / S) & 1)) return false;
+      ptx::tc_fence_after();
+      if (elect_one()) {
         product_nt<D>(tmem + 128u, sbase + C::kV, sbase + C::kDo + s * C::kTile);
         ptx::mma_commit(tfull);
-        ++nt;
-        return true;
-      };
-      for (long long at = st.lo; at < st.hi && ok;) {
-        long long u;
-        int t0, t1;
-        segment(at, u, t0, t1);
-        if (!wait(kvfull, nseg++ & 1) || !scores() || !tee()) break;
-        for (int t = t0; t < t1; ++t, ++n) {
-          const int s = (int)(n % S);
-          const bool more = t + 1 < t1;
-          if (!wait(pfull, n & 1)) { ok = false; break; }
-          ptx::tc_fence_after();
+      }
+      __syncwarp();
+      ++nt;
+      return true;
+    };
+    for (long long at = st.lo; at < st.hi && ok;) {
+      long long u;
+      int t0, t1;
+      segment(at, u, t0, t1);
+      if (!all_wait(kvfull, nseg++ & 1) || !scores() || !tee()) break;
+      for (int t = t0; t < t1; ++t, ++n) {
+        const int s = (int)(n % S);
+        const bool more = t + 1 < t1;
+        if (!all_wait(pfull, n & 1)) { ok = false; break; }
+        ptx::tc_fence_after();
+        if (elect_one()) {
           product_nn<D>(tmem + 256u, tmem, 64, sbase + C::kDo + s * C::kTile, t > t0);
           ptx::mma_commit(doempty(s));
-          if (more && !scores()) { ok = false; break; }
-          if (!wait(dsfull, n & 1)) { ok = false; break; }
-          ptx::tc_fence_after();
+        }
+        __syncwarp();
+        if (more && !scores()) { ok = false; break; }
+        if (!all_wait(dsfull, n & 1)) { ok = false; break; }
+        ptx::tc_fence_after();
+        if (elect_one()) {
           product_nn<D>(tmem + 256u + (uint32_t)D, tmem + 128u, 64, sbase + C::kQ + s * C::kTile, t > t0);
           ptx::mma_commit(qempty(s));
-          if (more && !tee()) { ok = false; break; }
+          if (!more) {
+            ptx::mma_commit(kvempty);
+            ptx::mma_commit(done);
+          }
         }
-        if (!ok) break;
-        ptx::mma_commit(kvempty);
-        ptx::mma_commit(done);
-        at += t1 - t0;
+        __syncwarp();
+        if (more && !tee()) { ok = false; break; }
       }
-      int zero = 0;                                 // never free TMEM under a running product
-      ptx::mma_commit(drain);
-      ptx::mbar_wait(drain, 0, &zero, a.err, kWaitLimit);
+      at += t1 - t0;
     }
+    int zero = 0;                                   // never free TMEM under a running product
+    if (elect_one()) ptx::mma_commit(drain);
+    ptx::mbar_wait(drain, 0, &zero, a.err, kWaitLimit);
   } else if (warp < 8) {
     // ------------------------------------------------------------- P, dS and the epilogue
     const int half = warp >> 2, row = threadIdx.x & 127;
@@ -730,21 +752,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The rest of dk and dv: sums of the parts of cut units, zeros for key tiles past an item's
-// last valid key. Grid: key tile, key head, item; a warp takes a key at a time.
+// last valid key. Grid: eighths of a key tile (16 keys), key tile, key head and item; a thread
+// has four neighbouring elements of dk and of dv.
 template <int D>
-__global__ void __launch_bounds__(256) cross_dkv_join_kernel(BwdArgs a, int grid) {
+__global__ void __launch_bounds__(16 * D / 4) cross_dkv_join_kernel(BwdArgs a, int grid) {
   const CrossGeom& g = a.g;
-  const int kt = blockIdx.x, hkv = blockIdx.y % g.Hkv, b = blockIdx.y / g.Hkv;
+  const int kt = blockIdx.y, hkv = blockIdx.z % g.Hkv, b = blockIdx.z / g.Hkv;
   const int nt = key_tiles(a, b);
-  const int lane = threadIdx.x & 31;
-  constexpr int V = D / 32;
+  const int r = blockIdx.x * 16 + threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4), key = kt * kCrossTile + r;
   int c0 = 0, c1 = -1;
-  long long u = 0, total = 0;
+  long long first = 0, total = 0;
   if (kt < nt) {
     const long long tiles = a.prefix ? a.prefix[g.B] : (long long)g.B * g.nkt;
     total = tiles * g.Hkv * g.nqt;
-    u = (a.prefix ? (long long)a.prefix[b] : (long long)b * g.nkt) * g.Hkv + (long long)hkv * nt + kt;
-    const long long first = u * g.nqt, last = first + g.nqt - 1;
+    const long long u = (a.prefix ? (long long)a.prefix[b] : (long long)b * g.nkt) * g.Hkv + (long long)hkv * nt + kt;
+    first = u * g.nqt;
+    const long long last = first + g.nqt - 1;
     c0 = (int)(first * grid / total);
     c1 = (int)(last * grid / total);
     while (c0 > 0 && total * c0 / grid > first) --c0;
@@ -753,28 +776,21 @@ __global__ void __launch_bounds__(256) cross_dkv_join_kernel(BwdArgs a, int grid
     while (total * (c1 + 1) / grid <= last) ++c1;
     if (c0 == c1) return;                           // written by its CTA
   }
-  for (int r = threadIdx.x >> 5; r < kCrossTile; r += 8) {
-    const int key = kt * kCrossTile + r;
-    if (key >= g.M) break;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      float s[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = 0.f;
-      for (int c = c0; c <= c1; ++c) {
-        const long long lo = total * c / grid;
-        if (lo == total * (c + 1) / grid) continue;   // fewer steps than CTAs: this one had none
-        // the unit is the CTA's first if the CTA starts inside it or at its start
-        const bool is_first = lo >= u * g.nqt;
-        const float* p = a.part + (((long long)(2 * c + (is_first ? 0 : 1)) * 2 + which) * kCrossTile + r) * D + lane * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[i] += p[i];
-      }
-      __nv_bfloat16* dst = (which ? a.dk : a.dv) + (((long long)b * g.M + key) * g.Hkv + hkv) * D + lane * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) dst[i] = __float2bfloat16_rn(s[i]);
-    }
+  if (key >= g.M) return;
+  float4 sv = make_float4(0.f, 0.f, 0.f, 0.f), sk = sv;
+  for (int c = c0; c <= c1; ++c) {
+    const long long lo = total * c / grid;
+    if (lo == total * (c + 1) / grid) continue;     // fewer steps than CTAs: this one had none
+    // the unit is the CTA's first if the CTA starts inside it or at its start
+    const int slot = 2 * c + (lo >= first ? 0 : 1);
+    const float4* p = reinterpret_cast<const float4*>(a.part) + ((long long)slot * 2 * kCrossTile + r) * (D / 4) + c4;
+    const float4 pv = p[0], pk = p[kCrossTile * (D / 4)];
+    sv.x += pv.x, sv.y += pv.y, sv.z += pv.z, sv.w += pv.w;
+    sk.x += pk.x, sk.y += pk.y, sk.z += pk.z, sk.w += pk.w;
   }
+  const long long at = (((long long)b * g.M + key) * g.Hkv + hkv) * D + 4 * c4;
+  *reinterpret_cast<uint2*>(a.dv + at) = make_uint2(pack_bf16x2(sv.x, sv.y), pack_bf16x2(sv.z, sv.w));
+  *reinterpret_cast<uint2*>(a.dk + at) = make_uint2(pack_bf16x2(sk.x, sk.y), pack_bf16x2(sk.z, sk.w));
 }
 
 // Row statistics: (lse / log 2, sum over the row of do out), one row of D elements by D/8 lanes. A
@@ -854,7 +870,7 @@ cudaError_t run_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtenso
   count_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cross_dkv_join_kernel<D><<<dim3(g.nkt, g.B * g.Hkv), 256, 0, s>>>(a, grid);
+  cross_dkv_join_kernel<D><<<dim3(8, g.nkt, g.B * g.Hkv), 16 * D / 4, 0, s>>>(a, grid);
   count_launches(1);
   return cudaGetLastError();
 }

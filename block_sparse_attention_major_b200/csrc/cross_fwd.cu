@@ -18,7 +18,7 @@
 // CTA roles (512 threads): warps 0-3 and 4-7 are the softmax of blocks A and B, a row (TMEM lane)
 // a thread; warps 8-11 write the finished blocks out (normalise, stage in shared memory, one
 // copy of the whole block); lane 0 of warp 12 loads Q and the K ring; warp 13 loads the V ring
-// and zeroes rows of masked keys; lane 0 of warp 14 issues all products. A block's scores are 128
+// and zeroes rows of masked keys; warp 14 issues all products. A block's scores are 128
 // TMEM columns, P overwrites them as bf16 pairs, and the block's next scores follow its P V in the
 // pipe's issue order. One thread issues for A and B in turn: that keeps the blocks half a period
 // apart, so that one multiplies while the other exponentiates (with an issuer for each, their
@@ -55,9 +55,9 @@ struct Cfg {
   static constexpr int kOut = kV + kStages * kTile;       // staging of one finished block
   static constexpr int kInv = kOut + kTile;               // [2][128] 1 / row sum
   static constexpr int kBar = kInv + 2 * kCrossTile * 4;
-  // kfull, kempty, vfull, vempty, vland [kStages each]; qfull, qempty, sfull, pfull, odone, lfull, oempty [2 each],
-  // drain
-  static constexpr int kBars = 5 * kStages + 15;
+  // kfull, kempty, vfull, vempty, vland [kStages each]; qfull, qempty, sfull, pfull (by half), odone, lfull,
+  // oempty [2 each]; drain
+  static constexpr int kBars = 5 * kStages + 17;
   static constexpr int kMisc = kBar + 8 * kBars;          // TMEM base, abort
   static constexpr int kSmem = 1024 + kMisc + 16;
   static_assert(kSmem <= 232448, "shared memory");
@@ -75,11 +75,11 @@ struct Bars {
   __device__ uint32_t qfull(int x) const { return b0 + 8 * (5 * S + x); }
   __device__ uint32_t qempty(int x) const { return b0 + 8 * (5 * S + 2 + x); }
   __device__ uint32_t sfull(int x) const { return b0 + 8 * (5 * S + 4 + x); }
-  __device__ uint32_t pfull(int x) const { return b0 + 8 * (5 * S + 6 + x); }
-  __device__ uint32_t odone(int x) const { return b0 + 8 * (5 * S + 8 + x); }
-  __device__ uint32_t lfull(int x) const { return b0 + 8 * (5 * S + 10 + x); }
-  __device__ uint32_t oempty(int x) const { return b0 + 8 * (5 * S + 12 + x); }
-  __device__ uint32_t drain() const { return b0 + 8 * (5 * S + 14); }
+  __device__ uint32_t pfull(int x, int half) const { return b0 + 8 * (5 * S + 6 + 2 * x + half); }
+  __device__ uint32_t odone(int x) const { return b0 + 8 * (5 * S + 10 + x); }
+  __device__ uint32_t lfull(int x) const { return b0 + 8 * (5 * S + 12 + x); }
+  __device__ uint32_t oempty(int x) const { return b0 + 8 * (5 * S + 14 + x); }
+  __device__ uint32_t drain() const { return b0 + 8 * (5 * S + 16); }
 };
 
 struct FwdArgs {
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar.qfull(x), 1);
       ptx::mbar_init(bar.qempty(x), 1);
       ptx::mbar_init(bar.sfull(x), 1);
-      ptx::mbar_init(bar.pfull(x), 4);        // one arrival per softmax warp
+      for (int h = 0; h < 2; ++h) ptx::mbar_init(bar.pfull(x, h), 4);     // one arrival per softmax warp
       ptx::mbar_init(bar.odone(x), 1);
       ptx::mbar_init(bar.lfull(x), 4);
       ptx::mbar_init(bar.oempty(x), 4);       // one per output warp
@@ -312,54 +312,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 14) {
       // ------------------------------------------------------------- MMA issuer
       // For each key tile, A and then B: P V of this tile, then the scores of the next (which
-      // may be the next unit's first).
-      if (lane == 0) {
-        uint32_t nk = 0, nv = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-        auto wait = [&](uint32_t b, uint32_t ph) { return ptx::mbar_wait(b, ph, abort, a.err, kWaitLimit); };
-        TileCursor cur, nxt;
-        nxt.rows[0] = nxt.rows[1] = 0;
-        nxt.open(a, blockIdx.x);
-        auto scores = [&](int x) {
-          const int s = (int)(nk % S);
-          if (nxt.kt == nxt.t0 && !wait(bar.qfull(x), nq[x]++ & 1)) return false;
-          if (!wait(bar.kfull(s), (nk / S) & 1)) return false;
-          ptx::tc_fence_after();
+      // may be the next unit's first). The warp runs whole; one lane issues.
+      uint32_t nk = 0, nv = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+      auto wait = [&](uint32_t b, uint32_t ph) { return warp_wait(b, ph, abort, a.err); };
+      TileCursor cur, nxt;
+      nxt.rows[0] = nxt.rows[1] = 0;
+      nxt.open(a, blockIdx.x);
+      auto scores = [&](int x) {
+        const int s = (int)(nk % S);
+        if (nxt.kt == nxt.t0 && !wait(bar.qfull(x), nq[x]++ & 1)) return false;
+        if (x == 0 && !wait(bar.kfull(s), (nk / S) & 1)) return false;
+        ptx::tc_fence_after();
+        const bool last = nxt.kt == nxt.t1 - 1, release = x == 1 || !nxt.has_b;
+        if (elect_one()) {
           product_nt<D>(tmem + 128u * (uint32_t)x, sbase + C::kQ + x * C::kTile, sbase + C::kK + s * C::kTile);
           ptx::mma_commit(bar.sfull(x));
-          if (nxt.kt == nxt.t1 - 1) ptx::mma_commit(bar.qempty(x));
-          if (x == 1 || !nxt.has_b) {
-            ptx::mma_commit(bar.kempty(s));
-            ++nk;
-          }
-          return true;
-        };
-        bool ok = !nxt.valid || (scores(0) && (!nxt.has_b || scores(1)));
-        while (ok && nxt.valid) {
-          cur = nxt;
-          nxt.next(a);
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (x == 0 || cur.has_b) {
-              const int s = (int)(nv % S);
-              // the unit before must have been read out of O
-              if (cur.kt == cur.t0 && cur.rows[x] > 1 && !wait(bar.oempty(x), cur.rows[x] & 1)) { ok = false; break; }
-              if (!wait(bar.vfull(s), (nv / S) & 1) || !wait(bar.pfull(x), np[x]++ & 1)) { ok = false; break; }
-              ptx::tc_fence_after();
-              product_nn<D>(tmem + 256u + (uint32_t)(x * D), tmem + 128u * (uint32_t)x, 32, sbase + C::kV + s * C::kTile,
-                            cur.kt > cur.t0);
-              if (cur.kt == cur.t1 - 1) ptx::mma_commit(bar.odone(x));
-              if (x == 1 || !cur.has_b) {
-                ptx::mma_commit(bar.vempty(s));
-                ++nv;
-              }
-            }
-            if (nxt.valid && (x == 0 || nxt.has_b)) ok = scores(x);
-          }
+          if (last) ptx::mma_commit(bar.qempty(x));
+          if (release) ptx::mma_commit(bar.kempty(s));
         }
-        // Never free TMEM under a running product.
-        int zero = 0;
-        ptx::mma_commit(bar.drain());
-        ptx::mbar_wait(bar.drain(), 0, &zero, a.err, kWaitLimit);
+        __syncwarp();
+        nk += release;
+        return true;
+      };
+      bool ok = !nxt.valid || (scores(0) && (!nxt.has_b || scores(1)));
+      while (ok && nxt.valid) {
+        cur = nxt;
+        nxt.next(a);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x == 0 || cur.has_b) {
+            const int s = (int)(nv % S);
+            // the unit before must have been read out of O
+            if (cur.kt == cur.t0 && cur.rows[x] > 1 && !wait(bar.oempty(x), cur.rows[x] & 1)) { ok = false; break; }
+            if (x == 0 && !wait(bar.vfull(s), (nv / S) & 1)) { ok = false; break; }
+            if (!wait(bar.pfull(x, 0), np[x] & 1)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint32_t o_tmem = tmem + 256u + (uint32_t)(x * D), p_tmem = tmem + 128u * (uint32_t)x;
+            const uint32_t v_smem = sbase + C::kV + s * C::kTile;
+            if (elect_one()) product_nn_half<D, 0>(o_tmem, p_tmem, 32, v_smem, cur.kt > cur.t0);
+            __syncwarp();
+            if (!wait(bar.pfull(x, 1), np[x]++ & 1)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const bool release = x == 1 || !cur.has_b;
+            if (elect_one()) {
+              product_nn_half<D, 1>(o_tmem, p_tmem, 32, v_smem, true);
+              if (cur.kt == cur.t1 - 1) ptx::mma_commit(bar.odone(x));
+              if (release) ptx::mma_commit(bar.vempty(s));
+            }
+            __syncwarp();
+            nv += release;
+          }
+          if (nxt.valid && (x == 0 || nxt.has_b) && !scores(x)) { ok = false; break; }
+        }
       }
+      // Never free TMEM under a running product.
+      int zero = 0;
+      if (elect_one()) ptx::mma_commit(bar.drain());
+      ptx::mbar_wait(bar.drain(), 0, &zero, a.err, kWaitLimit);
     }
   } else if (warp >= 8) {
     // --------------------------------------------------------------- output
@@ -482,22 +491,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float m = m_run == -INFINITY ? 0.0f : m_run;
         uint64_t sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-        if (full) {
+        // P goes to the issuer in two halves: the first 64 keys multiply V while the others are
+        // exponentiated
 #pragma unroll
-          for (int h = 0; h < 4; ++h) exp32<false>(&r[32 * h], 0u, c, m, sum, s_tmem + 16 * h);
-        } else {
-          exp32<true>(&r[0], w.x, c, m, sum, s_tmem);
-          exp32<true>(&r[32], w.y, c, m, sum, s_tmem + 16);
-          exp32<true>(&r[64], w.z, c, m, sum, s_tmem + 32);
-          exp32<true>(&r[96], w.w, c, m, sum, s_tmem + 48);
+        for (int h = 0; h < 2; ++h) {
+          if (full) {
+            exp32<false>(&r[64 * h], 0u, c, m, sum, s_tmem + 32 * h);
+            exp32<false>(&r[64 * h + 32], 0u, c, m, sum, s_tmem + 32 * h + 16);
+          } else {
+            exp32<true>(&r[64 * h], h ? w.z : w.x, c, m, sum, s_tmem + 32 * h);
+            exp32<true>(&r[64 * h + 32], h ? w.w : w.y, c, m, sum, s_tmem + 32 * h + 16);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar.pfull(x, h));
         }
         float s0, s1;
         uf2(fadd2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar.pfull(x));
       }
       if (!ok) break;
       // 1 / l for the output warps, once they have read the unit before; the lse from here
