@@ -149,6 +149,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c), "r"(h), "r"(n), "r"(b)
       : "memory");
 }
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c, int h, int n, int b) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c), "r"(h), "r"(n), "r"(b)
+               : "memory");
+}
 // The reverse copy; the part of the box outside the tensor is not written. Completion goes by
 // this thread's bulk groups: `store_read` waits until the shared memory may be written again.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c, int h, int n, int b) {

@@ -40,7 +40,7 @@ struct BwdArgs {
   const float2* stats;              // [B, H, N]: (lse / log 2, D); +inf for a row without a key
   const int* prefix;                // key tiles of the items before b; null: every item has nkt
   int kb_mul, vb_mul, qb_mul;
-  __nv_bfloat16 *dq, *dk, *dv;
+  __nv_bfloat16 *dk, *dv;
   float* part;                      // cut units: [CTA][first / last][dk, dv][128][D]
   uint32_t* err;
   float scale, scale_log2;
@@ -63,9 +63,11 @@ __device__ __forceinline__ float2 row_stats(const BwdArgs& a, int b, int hkv, in
 template <int D>
 struct CfgQ {
   static constexpr int kTile = kCrossTile * D * 2;
-  static constexpr int kKS = 3, kVS = 2;
+  // a key tile is held from its scores to its dq product, a value tile for one product only
+  static constexpr int kKS = 3, kVS = D == 128 ? 1 : 2;
   static constexpr int kQ = 0, kDo = kTile, kK = 2 * kTile, kV = kK + kKS * kTile;
-  static constexpr int kBar = kV + kVS * kTile;
+  static constexpr int kOut = kV + kVS * kTile;             // staging of a finished block
+  static constexpr int kBar = kOut + kTile;
   // kfull, kempty, kland [kKS]; vfull, vempty [kVS]; sfull [2]; qfull, qempty, dofull, doempty, tfull, dsfull,
   // done, drain
   static constexpr int kBars = 3 * kKS + 2 * kVS + 2 + 8;
@@ -77,8 +79,8 @@ struct CfgQ {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
-                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const BwdArgs a,
-                    int units) {
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmDq, const BwdArgs a, int units) {
   using C = CfgQ<D>;
   constexpr int KS = C::kKS, VS = C::kVS;
   extern __shared__ uint8_t smem_raw[];
@@ -132,6 +134,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         int qt, hkv, b;
         decode(u, qt, hkv, b);
         const int nt = key_tiles(a, b);
+        if (u + (int)gridDim.x < units) {           // the next unit's rows come from HBM meanwhile
+          int qf, hf, bf;
+          decode(u + (int)gridDim.x, qf, hf, bf);
+#pragma unroll
+          for (int cb = 0; cb < D / 64; ++cb) {
+            tma_prefetch_4d(&tmQ, cb * 64, hf * g.G, qf * g.tpt, bf * a.qb_mul);
+            tma_prefetch_4d(&tmDo, cb * 64, hf * g.G, qf * g.tpt, bf);
+          }
+        }
         if (nt == 0) continue;
         if (nq > 0 && !wait(qempty, (nq - 1) & 1)) break;
         ptx::mbar_arrive_expect_tx(qfull, bytes);
@@ -211,9 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nk > s) ptx::mbar_wait(kfull((int)s), ((nk - 1 - s) / KS) & 1, &zero, a.err, kWaitLimit);
   } else if (warp == 9) {
     // ------------------------------------------------------------- MMA issuer
-    // S(0), T(0); then for each tile: S of the next one (its buffer's dS went into the product two
-    // back, issued before), dq += dS K, T of the next one (T was read when dS was written). The
-    // warp runs whole; one lane issues.
+    // S(0), T(0), S(1); then, once a tile's dS is written: T of the next tile (this tile's was read
+    // for dS), dq += dS K, and S of the tile after (over this tile's dS). The next dS needs the
+    // first of the three only, so the others run under it. The warp runs whole; one lane issues.
     uint32_t ns = 0, nk = 0, nv = 0, nds = 0, nq = 0;
     bool ok = true;
     auto all_wait = [&](uint32_t b, uint32_t ph) { return warp_wait(b, ph, abort, a.err); };
@@ -251,11 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nt == 0) continue;
       if (!all_wait(qfull, nq & 1) || !scores(nt == 1)) break;
       if (!all_wait(dofull, nq & 1) || !tee(nt == 1)) break;
+      if (nt > 1 && !scores(nt == 2)) break;
       ++nq;
       for (int i = 0; i < nt; ++i) {
-        if (i + 1 < nt && !scores(i + 2 == nt)) { ok = false; break; }
         if (!all_wait(dsfull, nds++ & 1)) { ok = false; break; }
         ptx::tc_fence_after();
+        if (i + 1 < nt && !tee(i + 2 == nt)) { ok = false; break; }
         const int s = (int)(nk % KS);
         if (elect_one()) {
           product_nn<D>(tmem + 384u, tmem + 128u * (nk & 1), 64, sbase + C::kK + s * C::kTile, i > 0);
@@ -264,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++nk;
-        if (i + 1 < nt && !tee(i + 2 == nt)) { ok = false; break; }
+        if (i + 2 < nt && !scores(i + 3 == nt)) { ok = false; break; }
       }
     }
     int zero = 0;                                   // never free TMEM under a running product
@@ -272,16 +284,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_wait(drain, 0, &zero, a.err, kWaitLimit);
   } else if (warp < 8) {
     // ------------------------------------------------------------- dS and the epilogue
+    // A finished unit is written out between the probabilities and the dS of the next unit's
+    // first tile: its last product and the store run under them, and the accumulator is read
+    // before the dS that lets the next unit overwrite it.
     const int half = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float c = a.scale_log2;
     uint32_t n = 0, nd = 0;
     bool ok = true;
+    int held = -1;                                  // the unit whose gradient is still in the accumulator
+    // Waits for the last product of unit `from` (none if it has no key) and stores its block.
+    auto finish = [&](int from, bool any) {
+      bool in = !any || warp_wait(done, nd & 1, abort, a.err);
+      nd += any;
+      if (threadIdx.x == 0) store_read();           // the staging is free again
+      in = bar_all(1, 256, in);
+      if (!in) return false;
+      ptx::tc_fence_after();
+      const uint32_t o_tmem = tmem + 384u + (uint32_t)(half * (D / 2)) + lane_base;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 64; ++ch) {
+        uint32_t o[32], pk[16];
+        if (any) {
+          tmem_ld_x32(o_tmem + 32 * ch, o);
+          ptx::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          pk[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * a.scale, __uint_as_float(o[2 * k + 1]) * a.scale);
+        put_row32(smem + C::kOut, row, half * (D / 64) + ch, pk);
+      }
+      fence_proxy_async();
+      bar_sync(1, 256);
+      if (threadIdx.x == 0) {
+        int qt, hkv, b;
+        decode(from, qt, hkv, b);
+#pragma unroll
+        for (int cb = 0; cb < D / 64; ++cb)
+          tma_store_4d(&tmDq, sbase + C::kOut + cb * 16384, cb * 64, hkv * g.G, qt * g.tpt, b);
+        store_commit();
+      }
+      return true;
+    };
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       int qt, hkv, b;
       decode(u, qt, hkv, b);
       const int2 ik = item_keys(a.keys, b, g.M);
       const int nt = (ik.x + kCrossTile - 1) / kCrossTile;
+      if (nt == 0) {
+        if (held >= 0 && !finish(held, true)) break;
+        held = -1;
+        if (!finish(u, false)) break;
+        continue;
+      }
       const float2 st = row_stats(a, b, hkv, qt, row);
       const uint64_t cc = f2(c, c), mm = f2(-st.x, -st.x), dd = f2(-st.y, -st.y);
       for (int i = 0; i < nt; ++i, ++n) {
@@ -302,6 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uf2(ffma2(f2(__uint_as_float(p[2 * k]), __uint_as_float(p[2 * k + 1])), cc, mm), x0, x1);
           p[2 * k] = __float_as_uint(ex2(x0));
           p[2 * k + 1] = __float_as_uint(ex2(x1));
+        }
+        if (held >= 0) {
+          ok = finish(held, true);
+          held = -1;
+          if (!ok) break;
         }
         if (!warp_wait(tfull, n & 1, abort, a.err)) { ok = false; break; }
         ptx::tc_fence_after();
@@ -334,38 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(dsfull);
       }
       if (!ok) break;
-      if (nt > 0) {
-        if (!warp_wait(done, nd++ & 1, abort, a.err)) break;
-        ptx::tc_fence_after();
-      }
-      const int tok = qt * g.tpt + row / g.G, head = hkv * g.G + row % g.G;
-      const bool mine = row < g.G * g.tpt && tok < g.N;
-      __nv_bfloat16* out = a.dq + (((long long)b * g.N + tok) * g.H + head) * D + half * (D / 2);
-      const uint32_t o_tmem = tmem + 384u + (uint32_t)(half * (D / 2)) + lane_base;
-#pragma unroll 1
-      for (int ch = 0; ch < D / 64; ++ch) {
-        uint32_t o[32];
-        if (nt > 0) {
-          tmem_ld_x32(o_tmem + 32 * ch, o);
-          ptx::tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
-        }
-        if (!mine) continue;
-        uint4* dst = reinterpret_cast<uint4*>(out + 32 * ch);
-        const float sc = a.scale;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint4 v;
-          v.x = pack_bf16x2(__uint_as_float(o[8 * k + 0]) * sc, __uint_as_float(o[8 * k + 1]) * sc);
-          v.y = pack_bf16x2(__uint_as_float(o[8 * k + 2]) * sc, __uint_as_float(o[8 * k + 3]) * sc);
-          v.z = pack_bf16x2(__uint_as_float(o[8 * k + 4]) * sc, __uint_as_float(o[8 * k + 5]) * sc);
-          v.w = pack_bf16x2(__uint_as_float(o[8 * k + 6]) * sc, __uint_as_float(o[8 * k + 7]) * sc);
-          dst[k] = v;
-        }
-      }
+      held = u;
     }
+    if (ok && held >= 0) finish(held, true);
+    if (threadIdx.x == 0) store_done();
   }
 
   ptx::tc_fence_before();
@@ -793,16 +828,17 @@ __global__ void __launch_bounds__(16 * D / 4) cross_dkv_join_kernel(BwdArgs a, i
   *reinterpret_cast<uint2*>(a.dk + at) = make_uint2(pack_bf16x2(sk.x, sk.y), pack_bf16x2(sk.z, sk.w));
 }
 
-// Row statistics: (lse / log 2, sum over the row of do out), one row of D elements by D/8 lanes. A
-// row without a key gets lse = +inf, which makes its probabilities zero. Block 0 also writes the
+// Row statistics: (lse / log 2, sum over the row of do out), one row of D elements by D/8 lanes,
+// four rows a thread so that enough loads are in flight. A row without a key gets lse = +inf,
+// which makes its probabilities zero. Grid: rows of an item, item. One block also writes the
 // prefix sums of the items' key tiles.
 template <int D>
 __global__ void __launch_bounds__(256) cross_stats_kernel(CrossGeom g, KeySet keys, const __nv_bfloat16* __restrict__ out,
                                                           const __nv_bfloat16* __restrict__ dout,
                                                           const float* __restrict__ lse, float2* __restrict__ stats,
                                                           int* __restrict__ prefix) {
-  constexpr int L = D / 8;                          // lanes of a row
-  if (blockIdx.x == 0 && prefix && threadIdx.x < 32) {
+  constexpr int L = D / 8, kRows = 256 / L;         // lanes of a row; rows of a pass
+  if (blockIdx.x == 0 && blockIdx.y == 0 && prefix && threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int run = 0;
     for (int i0 = 0; i0 < g.B; i0 += 32) {
@@ -819,48 +855,58 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(CrossGeom g, KeySet ke
     }
     if (lane == 0) prefix[g.B] = run;
   }
-  const long long rows = (long long)g.B * g.N * g.H;
-  const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / L;
+  const uint32_t rows = (uint32_t)g.N * (uint32_t)g.H;      // of an item, below 2^31
+  const uint32_t r0 = blockIdx.x * (4u * kRows) + threadIdx.x / L;
   const int part = threadIdx.x % L;
-  float s = 0.f;
-  if (at < rows) {
-    const uint4 o = *reinterpret_cast<const uint4*>(out + at * D + part * 8);
-    const uint4 d = *reinterpret_cast<const uint4*>(dout + at * D + part * 8);
-    const uint32_t ov[4] = {o.x, o.y, o.z, o.w}, dv[4] = {d.x, d.y, d.z, d.w};
+  const long long item = (long long)blockIdx.y * rows;
+  uint4 o[4], d[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s += __uint_as_float(ov[i] << 16) * __uint_as_float(dv[i] << 16);
-      s += __uint_as_float(ov[i] & 0xffff0000u) * __uint_as_float(dv[i] & 0xffff0000u);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t r = r0 + (uint32_t)(i * kRows);
+    o[i] = d[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows) {
+      o[i] = *reinterpret_cast<const uint4*>(out + (item + r) * D + part * 8);
+      d[i] = *reinterpret_cast<const uint4*>(dout + (item + r) * D + part * 8);
     }
   }
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (part == 0 && at < rows) {
-    const int head = (int)(at % g.H);
-    const long long bn = at / g.H;
-    const int tok = (int)(bn % g.N), b = (int)(bn / g.N);
-    const long long i = ((long long)b * g.H + head) * g.N + tok;
-    const float z = lse[i];
-    stats[i] = z == -INFINITY ? make_float2(INFINITY, 0.f) : make_float2(z * 1.4426950408889634f, s);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t r = r0 + (uint32_t)(i * kRows);
+    const uint32_t ov[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, dv[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s += __uint_as_float(ov[k] << 16) * __uint_as_float(dv[k] << 16);
+      s += __uint_as_float(ov[k] & 0xffff0000u) * __uint_as_float(dv[k] & 0xffff0000u);
+    }
+#pragma unroll
+    for (int k = L / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (part == 0 && r < rows) {
+      const uint32_t tok = r / (uint32_t)g.H, head = r - tok * (uint32_t)g.H;
+      const long long at = ((long long)blockIdx.y * g.H + head) * g.N + tok;
+      const float z = lse[at];
+      stats[at] = z == -INFINITY ? make_float2(INFINITY, 0.f) : make_float2(z * 1.4426950408889634f, s);
+    }
   }
 }
 
 template <int D>
 cudaError_t run_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk, const CUtensorMap& mv,
-                    const BwdArgs& a, const __nv_bfloat16* out, const __nv_bfloat16* dout, const float* lse,
+                    const CUtensorMap& mdq, const BwdArgs& a, const __nv_bfloat16* out, const __nv_bfloat16* dout, const float* lse,
                     float2* stats, int* prefix, cudaStream_t s) {
   const CrossGeom& g = a.g;
   cudaError_t e = cudaFuncSetAttribute(cross_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgQ<D>::kSmem);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(cross_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgK<D>::kSmem);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)g.B * g.N * g.H, per = 256 / (D / 8);
-  cross_stats_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(g, a.keys, out, dout, lse, stats, prefix);
+  const long long rows = (long long)g.N * g.H, per = 4 * 256 / (D / 8);
+  cross_stats_kernel<D><<<dim3((unsigned)((rows + per - 1) / per), g.B), 256, 0, s>>>(g, a.keys, out, dout, lse, stats, prefix);
   count_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int units = g.B * g.Hkv * g.nqt;
-  cross_dq_kernel<D><<<units < kCrossSms ? units : kCrossSms, kThreads, CfgQ<D>::kSmem, s>>>(mq, mdo, mk, mv, a, units);
+  cross_dq_kernel<D><<<units < kCrossSms ? units : kCrossSms, kThreads, CfgQ<D>::kSmem, s>>>(mq, mdo, mk, mv, mdq, a,
+                                                                                               units);
   count_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -898,7 +944,6 @@ cudaError_t launch_cross_bwd(const CrossCall& c, const void* out, const float* l
   a.kb_mul = c.sk.b == 0 && g.B > 1 ? 0 : 1;
   a.vb_mul = c.sv.b == 0 && g.B > 1 ? 0 : 1;
   a.qb_mul = c.sq.b == 0 && g.B > 1 ? 0 : 1;
-  a.dq = static_cast<__nv_bfloat16*>(dq);
   a.dk = static_cast<__nv_bfloat16*>(dk);
   a.dv = static_cast<__nv_bfloat16*>(dv);
   a.part = reinterpret_cast<float*>(c.ws + w.part);
@@ -906,16 +951,17 @@ cudaError_t launch_cross_bwd(const CrossCall& c, const void* out, const float* l
   a.scale = c.scale;
   a.scale_log2 = c.scale * 1.4426950408889634f;
   const CrossStride dense = {(long long)g.N * g.H * g.d, (long long)g.H * g.d, g.d};
-  CUtensorMap mq, mdo, mk, mv;
+  CUtensorMap mq, mdo, mk, mv, mdq;
   if (!make_map_4d(&mq, c.q, g.d, g.H, g.N, g.B, c.sq, g.G, g.tpt) ||
       !make_map_4d(&mdo, dout, g.d, g.H, g.N, g.B, dense, g.G, g.tpt) ||
+      !make_map_4d(&mdq, dq, g.d, g.H, g.N, g.B, dense, g.G, g.tpt) ||
       !make_map_4d(&mk, c.k, g.d, g.Hkv, g.M, g.B, c.sk, 1, kCrossTile) ||
       !make_map_4d(&mv, c.v, g.d, g.Hkv, g.M, g.B, c.sv, 1, kCrossTile))
     return cudaErrorInvalidValue;
   const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(out);
   const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(dout);
-  return g.d == 128 ? run_bwd<128>(mq, mdo, mk, mv, a, o, d, lse, stats, prefix, s)
-                    : run_bwd<64>(mq, mdo, mk, mv, a, o, d, lse, stats, prefix, s);
+  return g.d == 128 ? run_bwd<128>(mq, mdo, mk, mv, mdq, a, o, d, lse, stats, prefix, s)
+                    : run_bwd<64>(mq, mdo, mk, mv, mdq, a, o, d, lse, stats, prefix, s);
 }
 
 }  // namespace bsa

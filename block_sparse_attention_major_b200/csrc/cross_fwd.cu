@@ -245,6 +245,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++nq[x];
             return true;
           };
+          // The next unit's queries come from HBM meanwhile: their buffers are free only when
+          // this unit's last scores are done.
+          if (u + (int)gridDim.x < a.units) {
+            const Unit f(a, u + (int)gridDim.x);
+            for (int x = 0; x < 2; ++x)
+              if (f.t0 < f.t1 && f.n0 + x * g.tpt < g.N)
+#pragma unroll
+                for (int cb = 0; cb < D / 64; ++cb)
+                  tma_prefetch_4d(&tmQ, cb * 64, f.hkv * g.G, f.n0 + x * g.tpt, f.b * a.qb_mul);
+          }
           for (int kt = t.t0; kt < t.t1 && ok; ++kt) {
             // Q_A, first key tile, Q_B, the other key tiles: what the first products need first
             if (kt == t.t0 && !load_q(0)) { ok = false; break; }
