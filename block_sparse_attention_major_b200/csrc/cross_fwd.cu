@@ -38,9 +38,9 @@ using namespace cross;
 
 constexpr int kThreads = 512;
 constexpr int kRegsLaunch = 128;
-constexpr int kRegsSoftmax = 184;
-constexpr int kRegsOut = 80;
-constexpr int kRegsControl = 64;
+constexpr int kRegsSoftmax = 176;
+constexpr int kRegsOut = 64;
+constexpr int kRegsControl = 96;
 static_assert(128 * (2 * kRegsSoftmax + kRegsOut + kRegsControl) <= kThreads * kRegsLaunch,
               "register split above the launch's pool");
 constexpr float kRescaleLog2 = 8.0f;     // O is rescaled only past 2^8 of growth
@@ -245,16 +245,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++nq[x];
             return true;
           };
-          // The next unit's queries come from HBM meanwhile: their buffers are free only when
-          // this unit's last scores are done.
-          if (u + (int)gridDim.x < a.units) {
-            const Unit f(a, u + (int)gridDim.x);
-            for (int x = 0; x < 2; ++x)
-              if (f.t0 < f.t1 && f.n0 + x * g.tpt < g.N)
-#pragma unroll
-                for (int cb = 0; cb < D / 64; ++cb)
-                  tma_prefetch_4d(&tmQ, cb * 64, f.hkv * g.G, f.n0 + x * g.tpt, f.b * a.qb_mul);
-          }
           for (int kt = t.t0; kt < t.t1 && ok; ++kt) {
             // Q_A, first key tile, Q_B, the other key tiles: what the first products need first
             if (kt == t.t0 && !load_q(0)) { ok = false; break; }
@@ -267,6 +257,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                           kt * kCrossTile, t.b * a.kb_mul);
             ++nk;
             if (kt == t.t0 && !load_q(1)) { ok = false; break; }
+              // The next unit's queries come from HBM meanwhile: their buffers are free only when
+              // this unit's last scores are done.
+              if (kt == t.t0 && u + (int)gridDim.x < a.units) {
+                const Unit f(a, u + (int)gridDim.x);
+                for (int x = 0; x < 2; ++x)
+                  if (f.t0 < f.t1 && f.n0 + x * g.tpt < g.N)
+#pragma unroll
+                    for (int cb = 0; cb < D / 64; ++cb)
+                      tma_prefetch_4d(&tmQ, cb * 64, f.hkv * g.G, f.n0 + x * g.tpt, f.b * a.qb_mul);
+              }
           }
         }
         // Never leave with copies in flight.
@@ -415,18 +415,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
           if (a.splits == 1) {
             uint32_t pk[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) pk[k] = pack_bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+            for (int k = 0; k < 16; ++k)
+              pk[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
             put_row32(stage, row, ch, pk);
           } else if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(
+            float4* dst = reinterpret_cast<float4*>(
                 a.part_o + ((((long long)t.part * g.B + t.b) * g.N + tok) * g.H + head) * D + 32 * ch);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                                   __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
           }
         }
         ptx::tc_fence_before();
