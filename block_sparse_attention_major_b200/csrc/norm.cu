@@ -15,20 +15,18 @@
 // Both passes are bound by HBM (2 C reads and writes a row forward, 3 C backward). Layout:
 // a thread holds slots of 8 elements (one 16-byte load of bf16, two of fp32), so a row of up
 // to 256 elements takes 8, 16 or 32 lanes and a block several rows, and a longer row takes a
-// block of its own (1 slot a thread to C = 5120, then 2 and 4). U rows a block are read before
-// the first is reduced, to keep enough bytes in flight. Rows whose width or address does not
+// block of its own, with 2 or 4 slots a thread. Each thread copies its own slots of
+// the next three groups of rows to shared memory while one group is at work: the bytes in
+// flight cost no registers and no barrier. Rows whose width or address does not
 // allow 16-byte loads take the same kernels with single-element, coalesced loads.
-// The grid is persistent: each block takes one contiguous range of rows, keeps w and b of the
-// item in registers, and in the backward pass the column sums of the rows it has seen. It
-// writes them as one partial row for each item that its range meets; a second kernel adds
+// The grid is persistent: each block takes one contiguous range of rows and in the backward pass
+// keeps the column sums of the rows it has seen. It writes them as one partial row for each item that its range meets; a second kernel adds
 // the partials of an item in the order of the blocks. No atomics: repeated calls give
 // identical bits.
 #include "common.cuh"
 
 namespace bsa {
 namespace {
-
-constexpr int kMaxVpt = 4;
 
 struct NormArgs {
   const void* x;
@@ -52,96 +50,120 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Column of element j of slot k of thread t: 8 neighbours a thread with 16-byte loads, else
-// neighbouring threads on neighbouring elements.
-template <bool VEC>
+// Column of element j of slot k of thread t: runs of E neighbouring elements a thread, E = 8 (16
+// bytes of bf16) or, where one side is fp32, 4 (16 bytes of that), or 1 where rows do not allow
+// wide accesses; neighbouring threads on neighbouring runs.
+template <int E>
 __device__ __forceinline__ int column(int t, int k, int j, int tpr) {
-  return VEC ? (t + k * tpr) * 8 + j : t + (k * 8 + j) * tpr;
+  return ((k * (8 / E) + j / E) * tpr + t) * E + j % E;
 }
+template <typename XT, typename YT, bool VEC>
+constexpr int kRun = !VEC ? 1 : sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
 
-// Eight elements of a row, as loaded.
-template <typename T, bool VEC>
+// Eight elements of a row in registers: from global memory one by one, or (E > 1) from the runs
+// that the thread has copied to shared memory.
+template <typename T, int E>
 struct Slot {
-  T v[8];
+  static constexpr int kWords = 2 * sizeof(T);      // 32-bit words
+  uint32_t v[kWords];
   __device__ __forceinline__ void load(const T* row, int t, int k, int tpr, int C, bool ok) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = column<VEC>(t, k, j, tpr);
-      v[j] = (ok && c < C) ? row[c] : T(0.f);
+      const int c = column<E>(t, k, j, tpr);
+      const float f = (ok && c < C) ? to_f(row[c]) : 0.f;
+      if (sizeof(T) == 4) v[j] = __float_as_uint(f);
+      else if (j & 1) v[j >> 1] |= __float_as_uint(f);
+      else v[j >> 1] = __float_as_uint(f) >> 16;
     }
   }
-  __device__ __forceinline__ float get(int j) const { return to_f(v[j]); }
-};
-template <>
-struct Slot<__nv_bfloat16, true> {
-  uint32_t v[4];
-  __device__ __forceinline__ void load(const __nv_bfloat16* row, int t, int k, int tpr, int C, bool ok) {
-    const int c = column<true>(t, k, 0, tpr);
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (ok && c < C) u = *reinterpret_cast<const uint4*>(row + c);
-    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+  __device__ __forceinline__ void take(const uint4* p, int plane) {
+    if (sizeof(T) == 2 && E == 4) {                 // two runs of 8 bytes in one 16-byte place
+      const uint2 a = reinterpret_cast<const uint2*>(p)[0], b = reinterpret_cast<const uint2*>(p)[1];
+      v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 u = p[i * plane];
+        v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+      }
+    }
   }
   __device__ __forceinline__ float get(int j) const {
+    if (sizeof(T) == 4) return __uint_as_float(v[j & (kWords - 1)]);
     return __uint_as_float((j & 1) ? (v[j >> 1] & 0xffff0000u) : (v[j >> 1] << 16));
   }
 };
-template <>
-struct Slot<float, true> {
-  float v[8];
-  __device__ __forceinline__ void load(const float* row, int t, int k, int tpr, int C, bool ok) {
-    const int c = column<true>(t, k, 0, tpr);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (ok && c < C) {
-      a = *reinterpret_cast<const float4*>(row + c);
-      b = *reinterpret_cast<const float4*>(row + c + 4);
-    }
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-  __device__ __forceinline__ float get(int j) const { return v[j]; }
-};
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_slot(T* row, int t, int k, int tpr, int C, const float (&o)[8]) {
-  if (VEC) {
-    const int c = column<true>(t, k, 0, tpr);
-    if (c >= C) return;
-    if (sizeof(T) == 2) {
-      uint32_t u[4];
+// 16-byte places of a slot, and the copy of one slot to the thread's own places in shared memory
+// (`plane` apart; zeros past the row's end or for a row that is not there). Nobody else reads
+// them, so waiting for one's own copies is all the ordering there is.
+template <typename T>
+constexpr int kPieces = sizeof(T) / 2;
+template <int E, typename T>
+__device__ __forceinline__ void copy_slot(uint4* dst, int plane, const T* row, int t, int k, int tpr, int C, bool ok) {
+  constexpr int kBytes = E * sizeof(T);
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&p);
-      }
-      *reinterpret_cast<uint4*>(row + c) = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
-      float4* d = reinterpret_cast<float4*>(row + c);
-      d[0] = make_float4(o[0], o[1], o[2], o[3]);
-      d[1] = make_float4(o[4], o[5], o[6], o[7]);
-    }
-  } else {
+  for (int i = 0; i < 8 / E; ++i) {
+    const int c = column<E>(t, k, i * E, tpr);
+    const bool in = ok && c < C;
+    const T* src = in ? row + c : row;
+    if (kBytes == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16 * i * plane), "l"(src), "r"(in ? 16 : 0)
+                   : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + 8 * i), "l"(src), "r"(in ? 8 : 0) : "memory");
+  }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int E, typename T>
+__device__ __forceinline__ void store_slot(T* row, int t, int k, int tpr, int C, const float (&o)[8]) {
+  if (E == 1) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = column<false>(t, k, j, tpr);
+      const int c = column<E>(t, k, j, tpr);
       if (c < C) put(row + c, o[j]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8 / E; ++i) {
+    const int c = column<E>(t, k, i * E, tpr);
+    if (c >= C) continue;
+    if (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(row + c) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    } else {
+      uint32_t u[4];
+#pragma unroll
+      for (int h = 0; h < E / 2; ++h) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(o[E * i + 2 * h], o[E * i + 2 * h + 1]);
+        u[h] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      if (E == 8) *reinterpret_cast<uint4*>(row + c) = make_uint4(u[0], u[1], u[2], u[3]);
+      else *reinterpret_cast<uint2*>(row + c) = make_uint2(u[0], u[1]);
     }
   }
 }
 
-// (offset +) w or b of this thread's columns, zero past C.
-template <bool VEC, int VPT>
+// (offset +) w or b of the columns of one slot, or `absent`; zero past C. Held in registers for an
+// item: read again for every group of rows they cost as much L2 traffic as the rows.
+template <int E>
 __device__ __forceinline__ void load_affine(const void* p, bool bf16, long long at, float add, float absent, int t,
-                                            int tpr, int C, float (&o)[VPT][8]) {
+                                            int k, int tpr, int C, float (&o)[8]) {
 #pragma unroll
-  for (int k = 0; k < VPT; ++k)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = column<VEC>(t, k, j, tpr);
-      float v = absent;
-      if (p && c < C)
-        v = add + (bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + c])
-                        : static_cast<const float*>(p)[at + c]);
-      o[k][j] = c < C ? v : 0.f;
-    }
+  for (int j = 0; j < 8; ++j) {
+    const int c = column<E>(t, k, j, tpr);
+    float v = absent;
+    if (p && c < C)
+      v = add + (bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + c])
+                      : static_cast<const float*>(p)[at + c]);
+    o[j] = c < C ? v : 0.f;
+  }
 }
 
 // Sums of S values over the threads of a row, left in every one of them. tpr <= 32: lanes of
@@ -169,26 +191,73 @@ __device__ __forceinline__ void row_sum(float (&s)[S], int tpr, float* red) {
   }
 }
 
-template <typename XT, typename YT, bool VEC, int VPT, int U, int T>
-__global__ void __launch_bounds__(T) norm_fwd_kernel(NormArgs a) {
+// Rows are taken in groups of U a lane group; all but one of a ring of groups are on their way to
+// shared memory while one is at work (VEC). Four groups, fewer where T threads' pieces of them
+// are over 200 KB.
+template <typename XT, int VPT, int U>
+constexpr int kFwdPieces = U* VPT* kPieces<XT>;
+template <typename XT, typename YT, int VPT, int U>
+constexpr int kBwdPieces = U* VPT*(kPieces<XT> + kPieces<YT>);
+constexpr int ring_depth(int pieces, int T) {
+  const int d = 204800 / (16 * pieces * T);
+  return d < 1 ? 1 : d > 4 ? 4 : d;
+}
+
+template <typename XT, typename YT, bool VEC, int VPT, int U, int T, int kPerSm>
+__global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
   __shared__ float red[2][U * 32];
+  extern __shared__ uint4 ring[];         // [kDepth][piece][thread]
+  constexpr int E = kRun<XT, YT, VEC>;
+  constexpr int P = kPieces<XT>, kDepth = ring_depth(kFwdPieces<XT, VPT, U>, T);
   const int tpr = a.tpr, t = threadIdx.x % tpr, sub = threadIdx.x / tpr, rpb = blockDim.x / tpr, C = a.C;
+  const int plane = blockDim.x;
   const float inv_c = 1.0f / (float)C;
   const XT* x = static_cast<const XT*>(a.x);
   YT* y = static_cast<YT*>(a.y);
   const long long lo = a.rows * blockIdx.x / gridDim.x, hi = a.rows * (blockIdx.x + 1) / gridDim.x;
+  const long long step = (long long)rpb * U;
   for (long long r0 = lo; r0 < hi;) {
-    const long long item = r0 / a.per, end = min(hi, (item + 1) * a.per);
+    const long long item = r0 / a.per, end = min(hi, (item + 1) * a.per), wat = a.w_items ? item * C : 0;
     float w[VPT][8], b[VPT][8];
-    load_affine<VEC, VPT>(a.w, a.w_bf16, a.w_items ? item * C : 0, a.offset, 1.f, t, tpr, C, w);
-    load_affine<VEC, VPT>(a.b, a.w_bf16, a.w_items ? item * C : 0, 0.f, 0.f, t, tpr, C, b);
-    for (long long base = r0; base < end; base += (long long)rpb * U) {
-      Slot<XT, VEC> xs[U][VPT];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const long long r = base + u * rpb + sub;
+    for (int k = 0; k < VPT; ++k) {
+      load_affine<E>(a.w, a.w_bf16, wat, a.offset, 1.f, t, k, tpr, C, w[k]);
+      load_affine<E>(a.b, a.w_bf16, wat, 0.f, 0.f, t, k, tpr, C, b[k]);
+    }
+    int put = 0, got = 0;                 // ring stages
+    auto request = [&](long long base) {
+      if (VEC) {
+        uint4* dst = ring + put * (kFwdPieces<XT, VPT, U> * plane) + threadIdx.x;
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) xs[u][k].load(x + (r < end ? r : base) * C, t, k, tpr, C, r < end);
+        for (int u = 0; u < U; ++u) {
+          const long long r = base + u * rpb + sub;
+#pragma unroll
+          for (int k = 0; k < VPT; ++k)
+            copy_slot<E>(dst + (u * VPT + k) * P * plane, plane, x + (r < end ? r : r0) * C, t, k, tpr, C, r < end);
+        }
+        copies_commit();
+        put = put + 1 == kDepth ? 0 : put + 1;
+      }
+    };
+    for (int i = 0; i < kDepth - 1; ++i) request(r0 + i * step);
+    for (long long base = r0; base < end; base += step) {
+      Slot<XT, E> xs[U][VPT];
+      request(base + (kDepth - 1) * step);
+      if constexpr (VEC) {
+        copies_wait<kDepth - 1>();
+        const uint4* src = ring + got * (kFwdPieces<XT, VPT, U> * plane) + threadIdx.x;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < VPT; ++k) xs[u][k].take(src + (u * VPT + k) * P * plane, plane);
+        got = got + 1 == kDepth ? 0 : got + 1;
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const long long r = base + u * rpb + sub;
+#pragma unroll
+          for (int k = 0; k < VPT; ++k) xs[u][k].load(x + (r < end ? r : base) * C, t, k, tpr, C, r < end);
+        }
       }
       float m[U], v[U];
 #pragma unroll
@@ -209,25 +278,28 @@ __global__ void __launch_bounds__(T) norm_fwd_kernel(NormArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float d = xs[u][k].get(j) - m[u];
-            v[u] += column<VEC>(t, k, j, tpr) < C ? d * d : 0.f;
+            v[u] += column<E>(t, k, j, tpr) < C ? d * d : 0.f;
           }
       }
       row_sum<U>(v, tpr, red[1]);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const long long r = base + u * rpb + sub;
-        if (r >= end) continue;
-        const float rs = 1.0f / sqrtf(v[u] * inv_c + a.eps);
-        if (t == 0) {
+        v[u] = 1.0f / sqrtf(v[u] * inv_c + a.eps);
+        if (t == 0 && r < end) {
           if (a.mean) a.mean[r] = m[u];
-          if (a.rstd) a.rstd[r] = rs;
+          if (a.rstd) a.rstd[r] = v[u];
         }
+      }
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
+      for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const long long r = base + u * rpb + sub;
           float o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = (xs[u][k].get(j) - m[u]) * rs * w[k][j] + b[k][j];
-          store_slot<VEC>(y + r * C, t, k, tpr, C, o);
+          for (int j = 0; j < 8; ++j) o[j] = (xs[u][k].get(j) - m[u]) * v[u] * w[k][j] + b[k][j];
+          if (r < end) store_slot<E>(y + r * C, t, k, tpr, C, o);
         }
       }
     }
@@ -235,72 +307,115 @@ __global__ void __launch_bounds__(T) norm_fwd_kernel(NormArgs a) {
   }
 }
 
-template <typename XT, typename YT, bool VEC, int VPT, int U, int T>
-__global__ void __launch_bounds__(T) norm_bwd_kernel(NormArgs a) {
+template <typename XT, typename YT, bool VEC, int VPT, int U, int T, int kPerSm>
+__global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
   __shared__ float red[2][2 * U * 32];
-  extern __shared__ float acc[];          // several rows a block: their column sums, [2][C]
+  extern __shared__ uint4 ring[];         // [kDepth][piece][thread]
+  constexpr int E = kRun<XT, YT, VEC>;
+  constexpr int PX = kPieces<XT>, PY = kPieces<YT>, kDepth = ring_depth(kBwdPieces<XT, YT, VPT, U>, T);
   const int tpr = a.tpr, t = threadIdx.x % tpr, sub = threadIdx.x / tpr, rpb = blockDim.x / tpr, C = a.C;
+  const int plane = blockDim.x;
   const float inv_c = 1.0f / (float)C;
   const XT* x = static_cast<const XT*>(a.x);
   const YT* dy = static_cast<const YT*>(a.dy);
   XT* dx = static_cast<XT*>(a.y);
+  // several rows a block: their column sums [2][C] meet here, behind the ring
+  float* acc = reinterpret_cast<float*>(ring + (VEC ? kDepth * kBwdPieces<XT, YT, VPT, U> * plane : 0));
   const long long lo = a.rows * blockIdx.x / gridDim.x, hi = a.rows * (blockIdx.x + 1) / gridDim.x;
+  const long long step = (long long)rpb * U;
   int flip = 0;
   for (long long r0 = lo; r0 < hi;) {
-    const long long item = r0 / a.per, end = min(hi, (item + 1) * a.per);
+    const long long item = r0 / a.per, end = min(hi, (item + 1) * a.per), wat = a.w_items ? item * C : 0;
     float w[VPT][8], dw[VPT][8], db[VPT][8];
-    load_affine<VEC, VPT>(a.w, a.w_bf16, a.w_items ? item * C : 0, a.offset, 1.f, t, tpr, C, w);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) load_affine<E>(a.w, a.w_bf16, wat, a.offset, 1.f, t, k, tpr, C, w[k]);
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.f;
-    for (long long base = r0; base < end; base += (long long)rpb * U) {
-      Slot<XT, VEC> xs[U][VPT];
-      Slot<YT, VEC> gs[U][VPT];
+    int put = 0, got = 0;                 // ring stages
+    auto request = [&](long long base) {
+      if (VEC) {
+        uint4* dst = ring + put * (kBwdPieces<XT, YT, VPT, U> * plane) + threadIdx.x;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const long long r = base + u * rpb + sub, q = r < end ? r : r0;
+#pragma unroll
+          for (int k = 0; k < VPT; ++k) {
+            copy_slot<E>(dst + (u * VPT + k) * (PX + PY) * plane, plane, x + q * C, t, k, tpr, C, r < end);
+            copy_slot<E>(dst + ((u * VPT + k) * (PX + PY) + PX) * plane, plane, dy + q * C, t, k, tpr, C, r < end);
+          }
+        }
+        copies_commit();
+        put = put + 1 == kDepth ? 0 : put + 1;
+      }
+    };
+    for (int i = 0; i < kDepth - 1; ++i) request(r0 + i * step);
+    for (long long base = r0; base < end; base += step) {
+      Slot<XT, E> xs[U][VPT];
+      Slot<YT, E> gs[U][VPT];
       float m[U], rs[U], s[2 * U];
+      request(base + (kDepth - 1) * step);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const long long r = base + u * rpb + sub, q = r < end ? r : base;
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-          xs[u][k].load(x + q * C, t, k, tpr, C, r < end);
-          gs[u][k].load(dy + q * C, t, k, tpr, C, r < end);
-        }
         m[u] = a.mean[q];
         rs[u] = a.rstd[q];
+        s[2 * u] = s[2 * u + 1] = 0.f;
+      }
+      if constexpr (VEC) {
+        copies_wait<kDepth - 1>();
+        const uint4* src = ring + got * (kBwdPieces<XT, YT, VPT, U> * plane) + threadIdx.x;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < VPT; ++k) {
+            xs[u][k].take(src + (u * VPT + k) * (PX + PY) * plane, plane);
+            gs[u][k].take(src + ((u * VPT + k) * (PX + PY) + PX) * plane, plane);
+          }
+        got = got + 1 == kDepth ? 0 : got + 1;
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const long long r = base + u * rpb + sub, q = r < end ? r : base;
+#pragma unroll
+          for (int k = 0; k < VPT; ++k) {
+            xs[u][k].load(x + q * C, t, k, tpr, C, r < end);
+            gs[u][k].load(dy + q * C, t, k, tpr, C, r < end);
+          }
+        }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        s[2 * u] = s[2 * u + 1] = 0.f;
+      for (int k = 0; k < VPT; ++k) {
 #pragma unroll
-        for (int k = 0; k < VPT; ++k)
+        for (int u = 0; u < U; ++u) {
+          const bool in = base + u * rpb + sub < end;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             // past the row's end dy is zero, so none of the sums sees the element
             const float d = gs[u][k].get(j), h = (xs[u][k].get(j) - m[u]) * rs[u], g = d * w[k][j];
             s[2 * u] += g;
             s[2 * u + 1] += g * h;
-            const bool in = base + u * rpb + sub < end;
             dw[k][j] += in ? d * h : 0.f;
             db[k][j] += d;
           }
+        }
       }
       row_sum<2 * U>(s, tpr, red[flip]);
       flip ^= 1;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const long long r = base + u * rpb + sub;
-        if (r >= end) continue;
-        const float c1 = s[2 * u] * inv_c, c2 = s[2 * u + 1] * inv_c;
+      for (int k = 0; k < VPT; ++k) {
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
+        for (int u = 0; u < U; ++u) {
+          const long long r = base + u * rpb + sub;
+          const float c1 = s[2 * u] * inv_c, c2 = s[2 * u + 1] * inv_c;
           float o[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float h = (xs[u][k].get(j) - m[u]) * rs[u];
             o[j] = rs[u] * (gs[u][k].get(j) * w[k][j] - c1 - h * c2);
           }
-          store_slot<VEC>(dx + r * C, t, k, tpr, C, o);
+          if (r < end) store_slot<E>(dx + r * C, t, k, tpr, C, o);
         }
       }
     }
@@ -314,7 +429,7 @@ __global__ void __launch_bounds__(T) norm_bwd_kernel(NormArgs a) {
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int c = column<VEC>(t, k, j, tpr);
+            const int c = column<E>(t, k, j, tpr);
             if (c < C) pw[c] = dw[k][j], pb[c] = db[k][j];
           }
       } else {
@@ -324,7 +439,7 @@ __global__ void __launch_bounds__(T) norm_bwd_kernel(NormArgs a) {
             for (int k = 0; k < VPT; ++k)
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const int c = column<VEC>(t, k, j, tpr);
+                const int c = column<E>(t, k, j, tpr);
                 if (c < C) {
                   acc[c] = g == 0 ? dw[k][j] : acc[c] + dw[k][j];
                   acc[C + c] = g == 0 ? db[k][j] : acc[C + c] + db[k][j];
@@ -371,54 +486,93 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
   if (threadIdx.x == 0 && cc < C) out[item * C + cc] = v;
 }
 
-// Threads of a row, slots a thread and threads of a block for a row of C elements.
+// Threads of a row, slots a thread and threads of a block for a row of C elements. More slots a
+// thread mean fewer warps a row, and the reductions, whose cost goes by the warp, are what a
+// block waits for (75600 rows of 5120 with 1 slot and 20 warps: 389 us); registers set the limit:
+// a slot takes 4 (bf16) or 8 of the row and 16 of w and b, or 24 of w, dw and db.
 struct NormShape {
   int tpr, vpt, threads;
 };
-NormShape norm_shape(int C) {
-  const int slots = ceil_div(C, 8);
+NormShape norm_shape(int C, bool bwd, bool fp32, bool vec) {
+  const int slots = ceil_div(C, 8), most = !vec ? 1 : bwd || fp32 ? 2 : 4;
   NormShape n;
-  n.vpt = 1;
-  if (slots <= 32) {
+  if (slots <= 32 * most) {                         // a warp or less
+    n.vpt = slots <= 32 ? 1 : slots <= 64 ? 2 : 4;
     n.tpr = slots <= 8 ? 8 : slots <= 16 ? 16 : 32;
     n.threads = 256;
     return n;
   }
-  n.vpt = slots <= 640 ? 1 : slots <= 1280 ? 2 : 4;
+  if (!vec) {                                       // no copies ahead: as many threads as go
+    n.vpt = slots <= 640 ? 1 : slots <= 1024 ? 2 : 4;
+  } else {                                          // the fewest lanes without work, then the fewest threads
+    n.vpt = most == 4 && 128 * ceil_div(slots, 128) <= 64 * ceil_div(slots, 64) ? 4 : 2;
+    if (slots > 1024) n.vpt = 4;
+  }
   n.threads = n.tpr = 32 * ceil_div(slots, 32 * n.vpt);
   return n;
 }
 
-constexpr int kNormU = 2;
 constexpr int kNormSms = 148;     // SMs of the part; the workspace is sized without asking the device
 
-// Blocks of a launch: enough to fill the device, never more than the rows give.
+// Rows that a lane group takes together: more make fewer reductions, fewer leave registers.
+template <typename XT, bool VEC, int VPT>
+constexpr int kFwdU = !VEC ? 1 : VPT == 1 ? 8 / sizeof(XT) : VPT == 2 ? 4 / sizeof(XT) : 1;
+template <bool VEC, int VPT>
+constexpr int kBwdU = VEC && VPT == 1 ? 2 : 1;
+
+// Blocks an SM that a kernel is built for: registers to hold everything (what does not fit goes
+// through L2, since the copies ahead leave L1 little: a backward pass with 216 bytes of it a
+// thread took twice as long).
+constexpr int per_sm(int vpt, int T) { return T > 256 ? 1 : vpt == 1 ? 3 : 2; }
+
+// Blocks of a launch: enough to fill the device, never more than there are rows for one each of a
+// block's lane groups.
 int norm_blocks(const NormShape& n, long long rows) {
-  const long long step = (long long)(n.threads / n.tpr) * kNormU;
-  const long long need = (rows + step - 1) / step;
-  const long long full = (long long)kNormSms * (1280 / n.threads > 1 ? 1280 / n.threads : 1);
+  const long long step = n.threads / n.tpr, need = (rows + step - 1) / step;
+  const int T = n.threads > 256 ? n.threads : 256;
+  const long long full = (long long)kNormSms * (per_sm(n.vpt, T) * T / n.threads);
   return (int)(need < full ? need : full);
 }
 
-template <typename XT, typename YT, bool VEC, int VPT, int T>
-cudaError_t run_norm(const NormArgs& a, bool bwd, const NormShape& n, int blocks, cudaStream_t s) {
-  if (bwd) {
-    const size_t acc = n.tpr < n.threads && a.part ? 2 * sizeof(float) * a.C : 0;
-    norm_bwd_kernel<XT, YT, VEC, VPT, kNormU, T><<<blocks, n.threads, acc, s>>>(a);
-  } else {
-    norm_fwd_kernel<XT, YT, VEC, VPT, kNormU, T><<<blocks, n.threads, 0, s>>>(a);
+template <typename Kernel>
+cudaError_t start(Kernel kernel, const NormArgs& a, int blocks, int threads, size_t smem, cudaStream_t s) {
+  if (smem > 40 * 1024) {       // above 48 KB with the static arrays
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
   }
+  kernel<<<blocks, threads, smem, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
 
-template <typename XT, typename YT>
-cudaError_t run_norm_v(const NormArgs& a, bool vec, bool bwd, const NormShape& n, int blocks, cudaStream_t s) {
-  if (n.vpt == 1)
-    return vec ? run_norm<XT, YT, true, 1, 640>(a, bwd, n, blocks, s) : run_norm<XT, YT, false, 1, 640>(a, bwd, n, blocks, s);
-  if (n.vpt == 2)
-    return vec ? run_norm<XT, YT, true, 2, 640>(a, bwd, n, blocks, s) : run_norm<XT, YT, false, 2, 640>(a, bwd, n, blocks, s);
-  return vec ? run_norm<XT, YT, true, 4, 512>(a, bwd, n, blocks, s) : run_norm<XT, YT, false, 4, 512>(a, bwd, n, blocks, s);
+template <typename XT, typename YT, bool VEC, int VPT, int T>
+cudaError_t run_fwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
+  constexpr int U = kFwdU<XT, VEC, VPT>, kPieces = kFwdPieces<XT, VPT, U>;
+  return start(norm_fwd_kernel<XT, YT, VEC, VPT, U, T, per_sm(VPT, T)>, a, blocks, n.threads,
+               VEC ? (size_t)16 * ring_depth(kPieces, T) * kPieces * n.threads : 0, s);
+}
+template <typename XT, typename YT, bool VEC, int VPT, int T>
+cudaError_t run_bwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
+  constexpr int U = kBwdU<VEC, VPT>, kPieces = kBwdPieces<XT, YT, VPT, U>;
+  return start(norm_bwd_kernel<XT, YT, VEC, VPT, U, T, per_sm(VPT, T)>, a, blocks, n.threads,
+               (VEC ? (size_t)16 * ring_depth(kPieces, T) * kPieces * n.threads : 0) +
+                   (n.tpr < n.threads && a.part ? 2 * sizeof(float) * a.C : 0),
+               s);
+}
+
+template <typename XT, typename YT, bool VEC, int VPT, int T>
+cudaError_t run_either(const NormArgs& a, bool bwd, const NormShape& n, int blocks, cudaStream_t s) {
+  return bwd ? run_bwd<XT, YT, VEC, VPT, T>(a, n, blocks, s) : run_fwd<XT, YT, VEC, VPT, T>(a, n, blocks, s);
+}
+template <typename XT, typename YT, bool VEC>
+cudaError_t run_norm(const NormArgs& a, bool bwd, const NormShape& n, int blocks, cudaStream_t s) {
+  const bool wide = n.threads > 256;
+  if (n.vpt == 1 && wide) return run_either<XT, YT, false, 1, 640>(a, bwd, n, blocks, s);   // rows without wide accesses only
+  if (n.vpt == 1) return run_either<XT, YT, VEC, 1, 256>(a, bwd, n, blocks, s);
+  if (n.vpt == 2 && wide) return run_either<XT, YT, VEC, 2, 512>(a, bwd, n, blocks, s);
+  if (n.vpt == 2) return run_either<XT, YT, VEC, 2, 256>(a, bwd, n, blocks, s);
+  if (wide) return run_either<XT, YT, VEC, 4, 512>(a, bwd, n, blocks, s);
+  return run_fwd<XT, YT, VEC, 4, 256>(a, n, blocks, s);       // the backward pass has 4 slots only past 256 threads
 }
 
 bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -436,24 +590,28 @@ NormArgs norm_args(const bsa_norm_shape& f) {
 }
 
 cudaError_t dispatch(const bsa_norm_shape& f, NormArgs& a, bool bwd, cudaStream_t s, int* blocks_out = nullptr) {
-  const NormShape n = norm_shape(f.C);
+  const bool vec = f.C % 8 == 0 && at16(a.x) && at16(a.y) && at16(a.dy);
+  const NormShape n = norm_shape(f.C, bwd, f.x_type == BSA_FP32, vec);
   const int blocks = norm_blocks(n, f.rows);
   a.tpr = n.tpr;
   a.slots = blocks + (a.w_items ? f.items : 1);
   if (blocks_out) *blocks_out = blocks;
-  const bool vec = f.C % 8 == 0 && at16(a.x) && at16(a.y) && at16(a.dy);
   const bool xb = f.x_type == BSA_BF16, yb = f.y_type == BSA_BF16;
-  if (xb && yb) return run_norm_v<__nv_bfloat16, __nv_bfloat16>(a, vec, bwd, n, blocks, s);
-  if (xb) return run_norm_v<__nv_bfloat16, float>(a, vec, bwd, n, blocks, s);
-  if (yb) return run_norm_v<float, __nv_bfloat16>(a, vec, bwd, n, blocks, s);
-  return run_norm_v<float, float>(a, vec, bwd, n, blocks, s);
+  if (xb && yb) return vec ? run_norm<__nv_bfloat16, __nv_bfloat16, true>(a, bwd, n, blocks, s) : run_norm<__nv_bfloat16, __nv_bfloat16, false>(a, bwd, n, blocks, s);
+  if (xb) return vec ? run_norm<__nv_bfloat16, float, true>(a, bwd, n, blocks, s) : run_norm<__nv_bfloat16, float, false>(a, bwd, n, blocks, s);
+  if (yb) return vec ? run_norm<float, __nv_bfloat16, true>(a, bwd, n, blocks, s) : run_norm<float, __nv_bfloat16, false>(a, bwd, n, blocks, s);
+  return vec ? run_norm<float, float, true>(a, bwd, n, blocks, s) : run_norm<float, float, false>(a, bwd, n, blocks, s);
 }
 
 }  // namespace
 
 size_t norm_workspace(const bsa_norm_shape& f) {
-  const long long slots = norm_blocks(norm_shape(f.C), f.rows) + (f.w_per_item ? f.items : 1);
-  return align256((size_t)slots * f.C * 2 * sizeof(float));
+  int blocks = 0;                 // whatever the addresses allow
+  for (const bool vec : {false, true}) {
+    const int n = norm_blocks(norm_shape(f.C, true, f.x_type == BSA_FP32, vec), f.rows);
+    if (n > blocks) blocks = n;
+  }
+  return align256((size_t)(blocks + (f.w_per_item ? f.items : 1)) * f.C * 2 * sizeof(float));
 }
 
 cudaError_t launch_norm_fwd(const bsa_norm_shape& f, const void* x, const void* w, const void* b, void* y,
