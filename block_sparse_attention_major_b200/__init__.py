@@ -17,6 +17,7 @@ Entry points (same names as the C ABI in include/bsa.h):
     cross_attn_fwd(g, q, k, v, kv_len, key_mask)    attention to an encoder's states of another
                                     length -> (out bf16 [B,N,H,d], lse fp32 [B,H,N])
     cross_attn_bwd(g, q, k, v, out, lse, dout, ...)    its gradients -> (dq, dk, dv)
+    cross_forward(g, q, k, v, ..., qk_norm)  the norm of Q and K per head, then that attention
     layer_norm_fwd(x, weight, bias)          -> (y, mean, rstd), over the last axis
     layer_norm_bwd(x, dy, mean, rstd, weight)    -> (dx, dweight, dbias)
 """
@@ -24,6 +25,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -509,7 +511,8 @@ def _need_strided(t: torch.Tensor, shape, name: str) -> None:
         raise ValueError(f"{name} must be contiguous in its last axis")
 
 
-def _cross_inputs(g: CrossGeometry, q, k, v, kv_len, key_mask) -> bsa_cross_strides:
+def _cross_inputs(g: CrossGeometry, q, k, v, kv_len, key_mask):
+    """Checks them; a reference to their strides, or None where they are dense."""
     _need_strided(q, (g.B, g.N, g.H, g.d), "q")
     _need_strided(k, (g.B, g.M, g.Hkv, g.d), "k")
     _need_strided(v, (g.B, g.M, g.Hkv, g.d), "v")
@@ -517,8 +520,10 @@ def _cross_inputs(g: CrossGeometry, q, k, v, kv_len, key_mask) -> bsa_cross_stri
         _need(kv_len, torch.int32, (g.B,), "kv_len")
     if key_mask is not None:
         _need(key_mask, torch.bool, (g.B, g.M), "key_mask")
+    if q.is_contiguous() and k.is_contiguous() and v.is_contiguous():
+        return None
     three = ctypes.c_longlong * 3
-    return bsa_cross_strides(*(three(*t.stride()[:3]) for t in (q, k, v)))
+    return ctypes.byref(bsa_cross_strides(*(three(*t.stride()[:3]) for t in (q, k, v))))
 
 
 def cross_attn_fwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -545,10 +550,9 @@ def cross_attn_fwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.
         _need(lse, torch.float32, (g.B, g.H, g.N), "lse")
     _need_ws(ws)
     sc = 1.0 / math.sqrt(g.d) if scale is None else float(scale)
-    _run("bsa_cross_attn_fwd", _device_of(q, k, v, kv_len, key_mask, out, lse, ws), stream,
-         lambda s: load_library().bsa_cross_attn_fwd(
-             ctypes.byref(g.c()), ctypes.byref(st), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(key_mask),
-             ctypes.c_float(sc), _ptr(out), _ptr(lse), _ptr(ws), ctypes.c_size_t(ws.numel()), s))
+    _call("bsa_cross_attn_fwd", (q, k, v, kv_len, key_mask, out, lse, ws), stream, load_library().bsa_cross_attn_fwd,
+          _cross_geom_ref(g), st, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(kv_len), _addr(key_mask), sc,
+          out.data_ptr(), _addr(lse), ws.data_ptr(), ws.numel())
     return out, lse
 
 
@@ -579,12 +583,32 @@ def cross_attn_bwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.
     _need(dv, torch.bfloat16, (g.B, g.M, g.Hkv, g.d), "dv")
     _need_ws(ws)
     sc = 1.0 / math.sqrt(g.d) if scale is None else float(scale)
-    _run("bsa_cross_attn_bwd", _device_of(q, k, v, out, lse, dout, kv_len, key_mask, dq, dk, dv, ws), stream,
-         lambda s: load_library().bsa_cross_attn_bwd(
-             ctypes.byref(g.c()), ctypes.byref(st), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
-             _ptr(kv_len), _ptr(key_mask), ctypes.c_float(sc), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
-             ctypes.c_size_t(ws.numel()), s))
+    _call("bsa_cross_attn_bwd", (q, k, v, out, lse, dout, kv_len, key_mask, dq, dk, dv, ws), stream,
+          load_library().bsa_cross_attn_bwd, _cross_geom_ref(g), st, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          out.data_ptr(), lse.data_ptr(), dout.data_ptr(), _addr(kv_len), _addr(key_mask), sc, dq.data_ptr(),
+          dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel())
     return dq, dk, dv
+
+
+def _call(what: str, tensors, stream, fn, *args) -> None:
+    """fn(*args, stream handle) on the one device of `tensors`, made current if it is not: _run for
+    the calls whose few microseconds of marshalling count."""
+    dev = _device_of(*tensors)
+    handle = _stream(stream, dev).value or 0
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, handle), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, handle), what)
+
+
+def _addr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=64)
+def _cross_geom_ref(g: CrossGeometry):
+    return ctypes.byref(g.c())
 
 
 _NORM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -649,9 +673,8 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t is not None:
             _need(t, torch.float32, x.shape[:-1], name)
-    _run("bsa_layer_norm_fwd", _device_of(x, weight, bias, y, mean, rstd), stream,
-         lambda s: load_library().bsa_layer_norm_fwd(ctypes.byref(f), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
-                                                     _ptr(mean), _ptr(rstd), s))
+    _call("bsa_layer_norm_fwd", (x, weight, bias, y, mean, rstd), stream, load_library().bsa_layer_norm_fwd,
+          ctypes.byref(f), x.data_ptr(), _addr(weight), _addr(bias), y.data_ptr(), _addr(mean), _addr(rstd))
     return y, mean, rstd
 
 
@@ -698,10 +721,10 @@ def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: 
             _need(t, torch.float32, weight.shape, name)
     if ws is not None:
         _need_ws(ws)
-    _run("bsa_layer_norm_bwd", _device_of(x, dy, mean, rstd, weight, dx, dweight, dbias, ws), stream,
-         lambda s: load_library().bsa_layer_norm_bwd(
-             ctypes.byref(f), _ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx), _ptr(dweight),
-             _ptr(dbias), _ptr(ws), ctypes.c_size_t(0 if ws is None else ws.numel()), s))
+    _call("bsa_layer_norm_bwd", (x, dy, mean, rstd, weight, dx, dweight, dbias, ws), stream,
+          load_library().bsa_layer_norm_bwd, ctypes.byref(f), x.data_ptr(), dy.data_ptr(), mean.data_ptr(),
+          rstd.data_ptr(), _addr(weight), dx.data_ptr(), _addr(dweight), _addr(dbias), _addr(ws),
+          0 if ws is None else ws.numel())
     return dx, dweight, dbias
 
 
@@ -723,9 +746,54 @@ class Buffers:
         self.ws = alloc_workspace(g, dev)
 
 
+@dataclass(frozen=True)
+class QKNorm:
+    """Layer norm of Q and K over the head dimension ahead of attention: weights and biases [d]
+    (bfloat16 or float32), shared by all heads and tokens; None for none."""
+
+    q_weight: torch.Tensor | None = None
+    q_bias: torch.Tensor | None = None
+    k_weight: torch.Tensor | None = None
+    k_bias: torch.Tensor | None = None
+    eps: float = 1e-6
+
+
+class CrossBuffers:
+    """Device buffers of one cross_forward call, allocated once and reused across calls."""
+
+    def __init__(self, g: CrossGeometry, qk_norm: bool = False, device=None):
+        dev = device or "cuda"
+        self.qn = torch.empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16, device=dev) if qk_norm else None
+        self.kn = torch.empty((g.B, g.M, g.Hkv, g.d), dtype=torch.bfloat16, device=dev) if qk_norm else None
+        self.out = torch.empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty((g.B, g.H, g.N), dtype=torch.float32, device=dev)
+        self.ws = alloc_cross_workspace(g, dev)
+
+
+def cross_forward(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                  kv_len: torch.Tensor | None = None, key_mask: torch.Tensor | None = None,
+                  qk_norm: QKNorm | None = None, bufs: CrossBuffers | None = None, scale: float | None = None,
+                  stream=None) -> CrossBuffers:
+    """The attention to an encoder's states as a block runs it: the norm of Q and K per head, if
+    any (q and k are then contiguous), and cross_attn_fwd. Returns the buffers; out and lse hold
+    the result."""
+    if bufs is None:
+        with _owned_by(stream):
+            bufs = CrossBuffers(g, qk_norm is not None, q.device)
+    if qk_norm is not None:
+        if bufs.qn is None:
+            raise ValueError("these buffers have no room for the norm: CrossBuffers(g, qk_norm=True)")
+        n = qk_norm
+        layer_norm_fwd(q, n.q_weight, n.q_bias, n.eps, y=bufs.qn, want_stats=False, stream=stream)
+        layer_norm_fwd(k, n.k_weight, n.k_bias, n.eps, y=bufs.kn, want_stats=False, stream=stream)
+        q, k = bufs.qn, bufs.kn
+    cross_attn_fwd(g, q, k, v, kv_len, key_mask, scale, bufs.out, bufs.lse, bufs.ws, stream=stream)
+    return bufs
+
+
 def forward(g: Geometry, p: MaskParams, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             difficulty: torch.Tensor, bufs: Buffers | None = None, scale: float | None = None,
-            stream=None, rebuild_mask: bool = True) -> Buffers:
+            stream=None, rebuild_mask: bool = True, qk_norm: QKNorm | None = None) -> Buffers:
     """The whole path: reorder Q, K, V; build the mask; block-sparse attention.
 
     Returns the buffers; out / lse hold the attention output and LSE in raster order.
@@ -736,17 +804,23 @@ def forward(g: Geometry, p: MaskParams, q: torch.Tensor, k: torch.Tensor, v: tor
     With window kind 2 (token-level circular support, radius p.radius in tokens) the
     attention masks the tokens outside each query token's support inside window tiles,
     with the route flags the mask build left in the workspace.
+    qk_norm: layer norm of Q and K over the head dimension first (the mask is then that of the
+    normalised Q and K).
     """
     if not rebuild_mask and bufs is None:
         raise ValueError("rebuild_mask=False attends through the mask held in bufs: pass the "
                          "Buffers of an earlier call")
     b = bufs or Buffers(g, q.device)
-    if rebuild_mask:
-        reorder_pool(g, q, b.qt, b.qbar, stream)
-        reorder_pool(g, k, b.kt, b.kbar, stream)
-    else:
-        reorder(g, q, b.qt, stream)
-        reorder(g, k, b.kt, stream)
+    for x, xt, xbar, norm in ((q, b.qt, b.qbar, qk_norm and (qk_norm.q_weight, qk_norm.q_bias)),
+                              (k, b.kt, b.kbar, qk_norm and (qk_norm.k_weight, qk_norm.k_bias))):
+        if qk_norm is not None:
+            # through `out`, which is not written before both have been reordered
+            _need(x, torch.bfloat16, (g.B, g.N, g.H, g.d), "q and k")
+            x, _, _ = layer_norm_fwd(x, *norm, qk_norm.eps, y=b.out, want_stats=False, stream=stream)
+        if rebuild_mask:
+            reorder_pool(g, x, xt, xbar, stream)
+        else:
+            reorder(g, x, xt, stream)
     reorder(g, v, b.vt, stream)
     if rebuild_mask:
         build_mask_pooled(g, p, b.qbar, b.kbar, difficulty, b.mask, b.kv_count, b.ws, stream)
@@ -761,6 +835,6 @@ def forward(g: Geometry, p: MaskParams, q: torch.Tensor, k: torch.Tensor, v: tor
 
 # kernels launched by forward(): 3 reorders (Q and K fused with their pooling when the
 # mask is rebuilt); route, score and select (plus entropy and budget in budget mode) unless
-# the mask is reused; 3 scheduler kernels and the attention kernel
-def launches_per_forward(p: MaskParams, rebuild_mask: bool = True) -> int:
-    return 3 + ((3 + (2 if p.budget_mode == 1 else 0)) if rebuild_mask else 0) + 4
+# the mask is reused; 3 scheduler kernels and the attention kernel; 2 norms with qk_norm
+def launches_per_forward(p: MaskParams, rebuild_mask: bool = True, qk_norm: bool = False) -> int:
+    return 3 + ((3 + (2 if p.budget_mode == 1 else 0)) if rebuild_mask else 0) + 4 + (2 if qk_norm else 0)

@@ -133,13 +133,19 @@ int check_cross(const bsa_cross_geom* g, const bsa_cross_strides* st, const void
 }
 
 int device_ok() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return BSA_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return BSA_ERR_CUDA;
-  if (major != 10 || minor != 0) return BSA_ERR_UNSUPPORTED_DEVICE;
-  return BSA_OK;
+  static OncePerDevice once;
+  int found = BSA_ERR_CUDA;
+  const cudaError_t e = once([&found] {
+    int dev = 0, major = 0, minor = 0;
+    cudaError_t r = cudaGetDevice(&dev);
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (r != cudaSuccess) return r;
+    if (major == 10 && minor == 0) return cudaSuccess;
+    found = BSA_ERR_UNSUPPORTED_DEVICE;
+    return cudaErrorInvalidDevice;
+  });
+  return e == cudaSuccess ? BSA_OK : found;
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA; }

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <stdint.h>
 
 #include "bsa.h"
@@ -113,6 +114,26 @@ __device__ __forceinline__ int tile_valid_count(const Geom& g, int tt, int ty, i
   return min(kTileEdge, g.T - tt * kTileEdge) * min(kTileEdge, g.Hs - ty * kTileEdge) *
          min(kTileEdge, g.Ws - tx * kTileEdge);
 }
+
+// Does something once for each device (of the first 64; each time on others), such as setting a
+// kernel's attributes there: what it sets stays, and asking again costs a launch's host time.
+class OncePerDevice {
+ public:
+  template <typename F>
+  cudaError_t operator()(F&& f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (bit & done_.load(std::memory_order_acquire)) return cudaSuccess;
+    e = f();
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
 
 // ------------------------------------------------------------------ error reporting
 __device__ __forceinline__ void report_error(uint32_t* err, uint32_t bits) {

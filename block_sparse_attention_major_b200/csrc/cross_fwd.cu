@@ -633,13 +633,18 @@ EncodeTiledFn encode_fn() {
 template <int D>
 cudaError_t run_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                     const FwdArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  static OncePerDevice once;
+  cudaError_t e = once([] {
+    cudaError_t r = cudaFuncSetAttribute(cross_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    if (r != cudaSuccess) return r;
+    // A register split above what the launch provides would wait forever in setmaxnreg.
+    cudaFuncAttributes fa;
+    r = cudaFuncGetAttributes(&fa, cross_fwd_kernel<D>);
+    if (r != cudaSuccess) return r;
+    return fa.numRegs * kThreads < 128 * (2 * kRegsSoftmax + kRegsOut + kRegsControl) ? cudaErrorInvalidConfiguration
+                                                                                    : cudaSuccess;
+  });
   if (e != cudaSuccess) return e;
-  // A register split above what the launch provides would wait forever in setmaxnreg.
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, cross_fwd_kernel<D>);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs * kThreads < 128 * (2 * kRegsSoftmax + kRegsOut + kRegsControl)) return cudaErrorInvalidConfiguration;
   cross_fwd_kernel<D><<<a.units < kCrossSms ? a.units : kCrossSms, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, mo, a);
   count_launches(1);
   e = cudaGetLastError();

@@ -534,13 +534,17 @@ int norm_blocks(const NormShape& n, long long rows) {
   return (int)(need < full ? need : full);
 }
 
-template <typename Kernel>
-cudaError_t start(Kernel kernel, const NormArgs& a, int blocks, int threads, size_t smem, cudaStream_t s) {
-  if (smem > 40 * 1024) {       // above 48 KB with the static arrays
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// `most`: the largest shared memory that a launch of this kernel takes (it needs leave above 48 KB,
+// static arrays included).
+template <auto kKernel>
+cudaError_t start(const NormArgs& a, int blocks, int threads, size_t smem, size_t most, cudaStream_t s) {
+  if (most > 40 * 1024) {
+    static OncePerDevice once;
+    const cudaError_t e =
+        once([most] { return cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most); });
     if (e != cudaSuccess) return e;
   }
-  kernel<<<blocks, threads, smem, s>>>(a);
+  kKernel<<<blocks, threads, smem, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -548,16 +552,17 @@ cudaError_t start(Kernel kernel, const NormArgs& a, int blocks, int threads, siz
 template <typename XT, typename YT, bool VEC, int VPT, int T>
 cudaError_t run_fwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
   constexpr int U = kFwdU<XT, VEC, VPT>, kPieces = kFwdPieces<XT, VPT, U>;
-  return start(norm_fwd_kernel<XT, YT, VEC, VPT, U, T, per_sm(VPT, T)>, a, blocks, n.threads,
-               VEC ? (size_t)16 * ring_depth(kPieces, T) * kPieces * n.threads : 0, s);
+  constexpr size_t kThread = VEC ? 16 * ring_depth(kPieces, T) * kPieces : 0;
+  return start<norm_fwd_kernel<XT, YT, VEC, VPT, U, T, per_sm(VPT, T)>>(a, blocks, n.threads, kThread * n.threads,
+                                                                        kThread * T, s);
 }
 template <typename XT, typename YT, bool VEC, int VPT, int T>
 cudaError_t run_bwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
   constexpr int U = kBwdU<VEC, VPT>, kPieces = kBwdPieces<XT, YT, VPT, U>;
-  return start(norm_bwd_kernel<XT, YT, VEC, VPT, U, T, per_sm(VPT, T)>, a, blocks, n.threads,
-               (VEC ? (size_t)16 * ring_depth(kPieces, T) * kPieces * n.threads : 0) +
-                   (n.tpr < n.threads && a.part ? 2 * sizeof(float) * a.C : 0),
-               s);
+  constexpr size_t kThread = VEC ? 16 * ring_depth(kPieces, T) * kPieces : 0;
+  const size_t acc = n.tpr < n.threads && a.part ? 2 * sizeof(float) * a.C : 0;      // rows of at most 512
+  return start<norm_bwd_kernel<XT, YT, VEC, VPT, U, T, per_sm(VPT, T)>>(
+      a, blocks, n.threads, kThread * n.threads + acc, kThread * T + 2 * sizeof(float) * 512, s);
 }
 
 template <typename XT, typename YT, bool VEC, int VPT, int T>
