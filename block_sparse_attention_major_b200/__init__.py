@@ -540,9 +540,9 @@ def cross_attn_fwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.
     dev = q.device
     with _owned_by(stream):
         if out is None:
-            out = torch.empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16, device=dev)
+            out = q.new_empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16)
         if want_lse and lse is None:
-            lse = torch.empty((g.B, g.H, g.N), dtype=torch.float32, device=dev)
+            lse = q.new_empty((g.B, g.H, g.N), dtype=torch.float32)
         if ws is None:
             ws = alloc_cross_workspace(g, dev)
     _need(out, torch.bfloat16, (g.B, g.N, g.H, g.d), "out")
@@ -571,11 +571,11 @@ def cross_attn_bwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.
     dev = q.device
     with _owned_by(stream):
         if dq is None:
-            dq = torch.empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16, device=dev)
+            dq = q.new_empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16)
         if dk is None:
-            dk = torch.empty((g.B, g.M, g.Hkv, g.d), dtype=torch.bfloat16, device=dev)
+            dk = q.new_empty((g.B, g.M, g.Hkv, g.d), dtype=torch.bfloat16)
         if dv is None:
-            dv = torch.empty((g.B, g.M, g.Hkv, g.d), dtype=torch.bfloat16, device=dev)
+            dv = q.new_empty((g.B, g.M, g.Hkv, g.d), dtype=torch.bfloat16)
         if ws is None:
             ws = alloc_cross_workspace(g, dev)
     _need(dq, torch.bfloat16, (g.B, g.N, g.H, g.d), "dq")
@@ -594,7 +594,10 @@ def _call(what: str, tensors, stream, fn, *args) -> None:
     """fn(*args, stream handle) on the one device of `tensors`, made current if it is not: _run for
     the calls whose few microseconds of marshalling count."""
     dev = _device_of(*tensors)
-    handle = _stream(stream, dev).value or 0
+    if stream is None and dev.type == "cuda":
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)    # without the Stream object, 2 us
+    else:
+        handle = _stream(stream, dev).value or 0
     if torch.cuda.current_device() == dev.index:
         _check(fn(*args, handle), what)
     else:
@@ -620,6 +623,11 @@ def _owned_by(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_struct(*fields) -> bsa_norm_shape:
+    return bsa_norm_shape(*fields)
+
+
 def _norm_shape(x, y_dtype, weight, bias, eps, weight_offset) -> bsa_norm_shape:
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
@@ -628,12 +636,11 @@ def _norm_shape(x, y_dtype, weight, bias, eps, weight_offset) -> bsa_norm_shape:
     if x.dim() < 1 or x.numel() == 0 or not x.is_contiguous():
         raise ValueError(f"x must be a contiguous [..., C] tensor with at least one row, got {tuple(x.shape)}")
     C = x.shape[-1]
-    f = bsa_norm_shape(x.numel() // C, C, 1, 0, _NORM_TYPES[x.dtype], _NORM_TYPES[y_dtype], 1, float(eps),
-                       float(weight_offset))
+    rows, xt, yt = x.numel() // C, _NORM_TYPES[x.dtype], _NORM_TYPES[y_dtype]
     if weight is None:
         if bias is not None:
             raise ValueError("a bias needs a weight of the same shape")
-        return f
+        return _norm_struct(rows, C, 1, 0, xt, yt, 1, float(eps), float(weight_offset))
     if not isinstance(weight, torch.Tensor) or weight.dtype not in _NORM_TYPES:
         raise ValueError("weight must be a bfloat16 or float32 tensor")
     shared, per_item = tuple(weight.shape) == (C,), x.dim() >= 2 and tuple(weight.shape) == (x.shape[0], C)
@@ -643,10 +650,8 @@ def _norm_shape(x, y_dtype, weight, bias, eps, weight_offset) -> bsa_norm_shape:
     _need(weight, weight.dtype, weight.shape, "weight")
     if bias is not None:
         _need(bias, weight.dtype, weight.shape, "bias")
-    f.w_type = _NORM_TYPES[weight.dtype]
-    if not shared:
-        f.w_per_item, f.items = 1, x.shape[0]
-    return f
+    return _norm_struct(rows, C, 1 if shared else x.shape[0], 0 if shared else 1, xt, yt, _NORM_TYPES[weight.dtype],
+                        float(eps), float(weight_offset))
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -664,11 +669,11 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     f = _norm_shape(x, dt, weight, bias, eps, weight_offset)
     with _owned_by(stream):
         if y is None:
-            y = torch.empty(x.shape, dtype=dt, device=x.device)
+            y = x.new_empty(x.shape, dtype=dt)
         if want_stats and mean is None:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+            mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
         if want_stats and rstd is None:
-            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+            rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
     _need(y, dt, x.shape, "y")
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t is not None:
@@ -708,11 +713,11 @@ def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: 
     want_bias = weight is not None and (want_bias or dbias is not None)
     with _owned_by(stream):
         if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            dx = x.new_empty(x.shape, dtype=x.dtype)
         if want_weight and dweight is None:
-            dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
+            dweight = x.new_empty(weight.shape, dtype=torch.float32)
         if want_bias and dbias is None:
-            dbias = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
+            dbias = x.new_empty(weight.shape, dtype=torch.float32)
         if ws is None and (want_weight or want_bias):
             ws = alloc_layer_norm_workspace(x, weight)
     _need(dx, x.dtype, x.shape, "dx")
