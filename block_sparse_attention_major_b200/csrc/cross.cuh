@@ -18,6 +18,7 @@ struct CrossGeom {
   int B, H, Hkv, d, N, M;
   int G, tpt;                        // query heads of a key head; tokens of a query tile
   int nqt, nkt;                      // query tiles (of one key head), key tiles
+  FastDiv by_hkv, by_G;
 };
 
 inline CrossGeom make_cross(const bsa_cross_geom& g) {
@@ -27,6 +28,8 @@ inline CrossGeom make_cross(const bsa_cross_geom& g) {
   c.tpt = kCrossTile / c.G;
   c.nqt = ceil_div(g.N, c.tpt);
   c.nkt = ceil_div(g.M, kCrossTile);
+  c.by_hkv = FastDiv((uint32_t)g.Hkv);
+  c.by_G = FastDiv((uint32_t)c.G);
   return c;
 }
 

@@ -44,6 +44,7 @@ struct BwdArgs {
   float* part;                      // cut units: [CTA][first / last][dk, dv][128][D]
   uint32_t* err;
   float scale, scale_log2;
+  FastDiv by_nqt;
 };
 
 __device__ __forceinline__ int key_tiles(const BwdArgs& a, int b) {
@@ -54,7 +55,7 @@ __device__ __forceinline__ int key_tiles(const BwdArgs& a, int b) {
 // take +inf: their probabilities are zero.
 __device__ __forceinline__ float2 row_stats(const BwdArgs& a, int b, int hkv, int qt, int r) {
   const CrossGeom& g = a.g;
-  const int tok = qt * g.tpt + r / g.G, head = hkv * g.G + r % g.G;
+  const int rt = (int)g.by_G.q((uint32_t)r), tok = qt * g.tpt + rt, head = hkv * g.G + r - rt * g.G;
   if (r >= g.G * g.tpt || tok >= g.N) return make_float2(INFINITY, 0.f);
   return a.stats[((long long)b * g.H + head) * g.N + tok];
 }
@@ -118,10 +119,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](uint32_t b, uint32_t ph) { return ptx::mbar_wait(b, ph, abort, a.err, kWaitLimit); };
   // unit -> (query tile, key head, item); query tiles fastest, so that neighbours share keys
   auto decode = [&](int u, int& qt, int& hkv, int& b) {
-    qt = u % g.nqt;
-    const int bh = u / g.nqt;
-    hkv = bh % g.Hkv;
-    b = bh / g.Hkv;
+    const int bh = (int)a.by_nqt.q((uint32_t)u);
+    qt = u - bh * g.nqt;
+    b = (int)g.by_hkv.q((uint32_t)bh);
+    hkv = bh - b * g.Hkv;
   };
 
   if (warp == 8) {
@@ -953,6 +954,7 @@ cudaError_t launch_cross_bwd(const CrossCall& c, const void* out, const float* l
   a.part = reinterpret_cast<float*>(c.ws + w.part);
   a.err = reinterpret_cast<uint32_t*>(c.ws);
   a.scale = c.scale;
+  a.by_nqt = FastDiv((uint32_t)g.nqt);
   a.scale_log2 = c.scale * 1.4426950408889634f;
   const CrossStride dense = {(long long)g.N * g.H * g.d, (long long)g.H * g.d, g.d};
   CUtensorMap mq, mdo, mk, mv, mdq;

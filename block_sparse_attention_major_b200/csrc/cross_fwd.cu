@@ -86,6 +86,7 @@ struct FwdArgs {
   CrossGeom g;
   KeySet keys;
   int units, splits, nqb;            // nqb: pairs of query tiles of a key head
+  FastDiv by_nqb, by_splits;
   int qb_mul, kb_mul, vb_mul;        // 0 where one item's tensor serves every item
   __nv_bfloat16* out;
   float* lse;
@@ -99,50 +100,46 @@ struct FwdArgs {
 struct Unit {
   int b, hkv, n0, part, t0, t1, len;
   __device__ __forceinline__ Unit(const FwdArgs& a, int u) {
-    const int qb = u % a.nqb, rest = u / a.nqb;
-    part = rest % a.splits;
-    const int bh = rest / a.splits;
-    hkv = bh % a.g.Hkv;
-    b = bh / a.g.Hkv;
-    n0 = qb * 2 * a.g.tpt;
+    const int rest = (int)a.by_nqb.q((uint32_t)u), bh = (int)a.by_splits.q((uint32_t)rest);
+    part = rest - bh * a.splits;
+    b = (int)a.g.by_hkv.q((uint32_t)bh);
+    hkv = bh - b * a.g.Hkv;
+    n0 = (u - rest * a.nqb) * 2 * a.g.tpt;
     len = item_keys(a.keys, b, a.g.M).x;
     const int nt = (len + kCrossTile - 1) / kCrossTile;
-    t0 = (int)((long long)nt * part / a.splits);
-    t1 = (int)((long long)nt * (part + 1) / a.splits);
+    t0 = 0;
+    t1 = nt;
+    if (a.splits > 1) {
+      t0 = (int)((long long)nt * part / a.splits);
+      t1 = (int)((long long)nt * (part + 1) / a.splits);
+    }
   }
 };
 
-// Row maximum over 32 columns, of the slots in `w` if masked, in four chains.
-template <bool kMasked>
-__device__ __forceinline__ void max32(const uint32_t* r, uint32_t w, float (&m)[4]) {
+// Scores of masked keys (clear bits of `w`) become -inf, whatever they were: the maximum and the
+// exponentials then need no mask.
+__device__ __forceinline__ void mask32(uint32_t* r, uint32_t w) {
 #pragma unroll
-  for (int c = 0; c < 32; c += 8) {
+  for (int c = 0; c < 32; ++c) r[c] = ((w >> c) & 1u) ? r[c] : 0xff800000u;
+}
+
+// Row maximum over 32 columns, in four chains.
+__device__ __forceinline__ void max32(const uint32_t* r, float (&m)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float u = __uint_as_float(r[c + 2 * j]), v = __uint_as_float(r[c + 2 * j + 1]);
-      if (kMasked) {
-        u = ((w >> (c + 2 * j)) & 1u) ? u : -INFINITY;
-        v = ((w >> (c + 2 * j + 1)) & 1u) ? v : -INFINITY;
-      }
-      m[j] = max3(m[j], u, v);
-    }
-  }
+  for (int c = 0; c < 32; c += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = max3(m[j], __uint_as_float(r[c + 2 * j]), __uint_as_float(r[c + 2 * j + 1]));
 }
 
 // p = 2^(c s - m) of 32 columns, stored as 16 columns of bf16 pairs; their fp32 sum joins `sum`.
-template <bool kMasked>
-__device__ __forceinline__ void exp32(const uint32_t* r, uint32_t w, float c, float m, uint64_t (&sum)[2], uint32_t taddr) {
+__device__ __forceinline__ void exp32(const uint32_t* r, float c, float m, uint64_t (&sum)[2], uint32_t taddr) {
   const uint64_t cc = f2(c, c), mm = f2(-m, -m);
   uint32_t pk[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float x0, x1;
     uf2(ffma2(f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), cc, mm), x0, x1);
-    float p0 = ex2(x0), p1 = ex2(x1);
-    if (kMasked) {
-      p0 = ((w >> (2 * i)) & 1u) ? p0 : 0.f;
-      p1 = ((w >> (2 * i + 1)) & 1u) ? p1 : 0.f;
-    }
+    const float p0 = ex2(x0), p1 = ex2(x1);
     pk[i] = pack_bf16x2(p0, p1);
     sum[i & 1] = fadd2(sum[i & 1], f2(p0, p1));
   }
@@ -385,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::setmaxnreg_dec<kRegsOut>();
     const int row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int row_tok = (int)g.by_G.q((uint32_t)row), row_head = row - row_tok * g.G;
     uint8_t* stage = smem + C::kOut;
     uint32_t nl[2] = {0, 0}, no[2] = {0, 0};
     bool ok = true;
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         const float inv = s_inv[x * kCrossTile + row];
         const uint32_t o_tmem = tmem + 256u + (uint32_t)(x * D) + lane_base;
-        const int tok = first + row / g.G, head = t.hkv * g.G + row % g.G;
+        const int tok = first + row_tok, head = t.hkv * g.G + row_head;
         const bool mine = row < g.G * g.tpt && tok < g.N;
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
@@ -453,11 +451,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + 128u * (uint32_t)x + lane_base;
     const uint32_t o_tmem = tmem + 256u + (uint32_t)(x * D) + lane_base;
+    const int row_tok = (int)g.by_G.q((uint32_t)row), row_head = row - row_tok * g.G;
     const float c = a.scale_log2;
     uint32_t ns = 0, nu = 0;
     bool ok = true;
+    Unit ahead(a, (int)blockIdx.x < a.units ? blockIdx.x : 0);
     for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-      const Unit t(a, u);
+      const Unit t = ahead;
+      const int after = u + (int)gridDim.x;
+      if (t.t0 == t.t1 || t.n0 + x * g.tpt >= g.N) ahead = Unit(a, after < a.units ? after : 0);
       const int first = t.n0 + x * g.tpt;
       if (first >= g.N) continue;
       float m_run = -INFINITY, l = 0.f;
@@ -469,17 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < 4; ++h) tmem_ld_x32(s_tmem + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * h]));
         ptx::tmem_wait_ld();
-        const bool full = all_set(w);
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (full) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) max32<false>(&r[32 * h], 0u, mx);
-        } else {
-          max32<true>(&r[0], w.x, mx);
-          max32<true>(&r[32], w.y, mx);
-          max32<true>(&r[64], w.z, mx);
-          max32<true>(&r[96], w.w, mx);
+        if (!all_set(w)) {
+          mask32(&r[0], w.x);
+          mask32(&r[32], w.y);
+          mask32(&r[64], w.z);
+          mask32(&r[96], w.w);
         }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) max32(&r[32 * h], mx);
         const float mb = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
         bool resc = false;
         if (m_run == -INFINITY) m_run = mb;            // nothing of this row is in O yet but zeros
@@ -506,18 +506,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // exponentiated
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (full) {
-            exp32<false>(&r[64 * h], 0u, c, m, sum, s_tmem + 32 * h);
-            exp32<false>(&r[64 * h + 32], 0u, c, m, sum, s_tmem + 32 * h + 16);
-          } else {
-            exp32<true>(&r[64 * h], h ? w.z : w.x, c, m, sum, s_tmem + 32 * h);
-            exp32<true>(&r[64 * h + 32], h ? w.w : w.y, c, m, sum, s_tmem + 32 * h + 16);
-          }
+          exp32(&r[64 * h], c, m, sum, s_tmem + 32 * h);
+          exp32(&r[64 * h + 32], c, m, sum, s_tmem + 32 * h + 16);
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar.pfull(x, h));
         }
+        // what the next unit is, under this one's products
+        if (kt == t.t0) ahead = Unit(a, after < a.units ? after : 0);
         float s0, s1;
         uf2(fadd2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
@@ -529,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       s_inv[x * kCrossTile + row] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : NAN);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar.lfull(x));
-      const int tok = first + row / g.G, head = t.hkv * g.G + row % g.G;
+      const int tok = first + row_tok, head = t.hkv * g.G + row_head;
       if (row < g.G * g.tpt && tok < g.N) {
         const float lse2 = l > 0.f ? (m_run == -INFINITY ? 0.0f : m_run) + __log2f(l) : (l == 0.f ? -INFINITY : NAN);
         const long long at = ((long long)t.b * g.H + head) * g.N + tok;
@@ -697,6 +694,8 @@ cudaError_t launch_cross_fwd(const CrossCall& c, void* out, float* lse, cudaStre
   }
   a.splits = cross_splits(g);
   a.nqb = ceil_div(g.nqt, 2);
+  a.by_nqb = FastDiv((uint32_t)a.nqb);
+  a.by_splits = FastDiv((uint32_t)a.splits);
   a.units = g.B * g.Hkv * a.splits * a.nqb;
   a.qb_mul = c.sq.b == 0 && g.B > 1 ? 0 : 1;
   a.kb_mul = c.sk.b == 0 && g.B > 1 ? 0 : 1;
