@@ -97,7 +97,23 @@ inline CrossWs cross_ws(const CrossGeom& g) {
 // ------------------------------------------------------------------------ device helpers
 namespace cross {
 
-constexpr long long kWaitLimit = 4000000000LL;     // SM cycles, about 2 s
+// Bounded wait for the phase of parity `parity`: each try suspends the thread for at most 200 ns, so
+// giving up takes between a tenth of a second and some two seconds. Gives up at once when another
+// thread has set *abort; on time-out it sets *abort and the error bit. Kept short because it
+// stands at every hand-over of warps that run little else: with a clock in it, the code of the
+// waits alone displaced the others' from the instruction cache.
+constexpr int kWaitTries = 1 << 23;
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < kWaitTries; ++i) {
+    if (ptx::mbar_try_wait_ns(bar, parity, 200)) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  atomicOr(err, BSA_KERR_WAIT_TIMEOUT);
+  return false;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -140,7 +156,7 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
 
 // All lanes take the same decision after a per-thread bounded wait.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, err, kWaitLimit));
+  return __all_sync(0xffffffffu, wait_phase(bar, parity, abort, err));
 }
 
 // Box of a 4-D map (columns, heads, tokens, items) into shared memory.

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;                 // S buffers at 0 and 128, T at 256, dq at 384
 
-  auto wait = [&](uint32_t b, uint32_t ph) { return ptx::mbar_wait(b, ph, abort, a.err, kWaitLimit); };
+  auto wait = [&](uint32_t b, uint32_t ph) { return wait_phase(b, ph, abort, a.err); };
   // unit -> (query tile, key head, item); query tiles fastest, so that neighbours share keys
   auto decode = [&](int u, int& qt, int& hkv, int& b) {
     const int bh = (int)a.by_nqt.q((uint32_t)u);
@@ -173,10 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       int zero = 0;                                 // never leave with copies in flight
       for (uint32_t s = 0; s < VS; ++s)
-        if (nv > s) ptx::mbar_wait(vfull((int)s), ((nv - 1 - s) / VS) & 1, &zero, a.err, kWaitLimit);
+        if (nv > s) wait_phase(vfull((int)s), ((nv - 1 - s) / VS) & 1, &zero, a.err);
       if (nq > 0) {
-        ptx::mbar_wait(qfull, (nq - 1) & 1, &zero, a.err, kWaitLimit);
-        ptx::mbar_wait(dofull, (nq - 1) & 1, &zero, a.err, kWaitLimit);
+        wait_phase(qfull, (nq - 1) & 1, &zero, a.err);
+        wait_phase(dofull, (nq - 1) & 1, &zero, a.err);
       }
     }
   } else if (warp == 10) {
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < KS; ++j)
             if (j == s) ph = land[j]++ & 1;
           int zero = 0;
-          const bool in = __all_sync(0xffffffffu, ptx::mbar_wait(kland(s), ph, &zero, a.err, kWaitLimit));
+          const bool in = __all_sync(0xffffffffu, wait_phase(kland(s), ph, &zero, a.err));
           if (!in) { *abort = 1; ok = false; break; }
           zero_masked_rows<D>(smem + C::kK + s * C::kTile, w, lane);
           if (lane == 0) ptx::mbar_arrive(kfull(s));
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int zero = 0;
     for (uint32_t s = 0; s < KS; ++s)
-      if (nk > s) ptx::mbar_wait(kfull((int)s), ((nk - 1 - s) / KS) & 1, &zero, a.err, kWaitLimit);
+      if (nk > s) wait_phase(kfull((int)s), ((nk - 1 - s) / KS) & 1, &zero, a.err);
   } else if (warp == 9) {
     // ------------------------------------------------------------- MMA issuer
     // S(0), T(0), S(1); then, once a tile's dS is written: T of the next tile (this tile's was read
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int zero = 0;                                   // never free TMEM under a running product
     if (elect_one()) ptx::mma_commit(drain);
-    ptx::mbar_wait(drain, 0, &zero, a.err, kWaitLimit);
+    wait_phase(drain, 0, &zero, a.err);
   } else if (warp < 8) {
     // ------------------------------------------------------------- dS and the epilogue
     // A finished unit is written out between the probabilities and the dS of the next unit's
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;                 // S^T at 0, T^T at 128, dv at 256, dk at 256 + D
 
   const Steps st(a, blockIdx.x, gridDim.x);
-  auto wait = [&](uint32_t b, uint32_t ph) { return ptx::mbar_wait(b, ph, abort, a.err, kWaitLimit); };
+  auto wait = [&](uint32_t b, uint32_t ph) { return wait_phase(b, ph, abort, a.err); };
   // Segments of this CTA's range: unit u, query tiles [t0, t1).
   auto segment = [&](long long at, long long& u, int& t0, int& t1) {
     u = at / g.nqt;
@@ -559,10 +559,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       int zero = 0;                                 // never leave with copies in flight
       for (uint32_t s = 0; s < S; ++s) {
-        if (nq > s) ptx::mbar_wait(qfull((int)s), ((nq - 1 - s) / S) & 1, &zero, a.err, kWaitLimit);
-        if (nd > s) ptx::mbar_wait(dofull((int)s), ((nd - 1 - s) / S) & 1, &zero, a.err, kWaitLimit);
+        if (nq > s) wait_phase(qfull((int)s), ((nq - 1 - s) / S) & 1, &zero, a.err);
+        if (nd > s) wait_phase(dofull((int)s), ((nd - 1 - s) / S) & 1, &zero, a.err);
       }
-      if (nseg > 0) ptx::mbar_wait(kvfull, (nseg - 1) & 1, &zero, a.err, kWaitLimit);
+      if (nseg > 0) wait_phase(kvfull, (nseg - 1) & 1, &zero, a.err);
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------- row statistics
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int zero = 0;                                   // never free TMEM under a running product
     if (elect_one()) ptx::mma_commit(drain);
-    ptx::mbar_wait(drain, 0, &zero, a.err, kWaitLimit);
+    wait_phase(drain, 0, &zero, a.err);
   } else if (warp < 8) {
     // ------------------------------------------------------------- P, dS and the epilogue
     const int half = warp >> 2, row = threadIdx.x & 127;

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto load_q = [&](int x) {
             const int n = t.n0 + x * g.tpt;
             if (n >= g.N) return true;
-            if (nq[x] > 0 && !ptx::mbar_wait(bar.qempty(x), (nq[x] - 1) & 1, abort, a.err, kWaitLimit)) return false;
+            if (nq[x] > 0 && !wait_phase(bar.qempty(x), (nq[x] - 1) & 1, abort, a.err)) return false;
             ptx::mbar_arrive_expect_tx(bar.qfull(x), qbytes);
 #pragma unroll
             for (int cb = 0; cb < D / 64; ++cb)
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Q_A, first key tile, Q_B, the other key tiles: what the first products need first
             if (kt == t.t0 && !load_q(0)) { ok = false; break; }
             const int s = (int)(nk % S);
-            if (!ptx::mbar_wait(bar.kempty(s), ((nk / S) & 1) ^ 1, abort, a.err, kWaitLimit)) { ok = false; break; }
+            if (!wait_phase(bar.kempty(s), ((nk / S) & 1) ^ 1, abort, a.err)) { ok = false; break; }
             ptx::mbar_arrive_expect_tx(bar.kfull(s), C::kTile);
 #pragma unroll
             for (int cb = 0; cb < D / 64; ++cb)
@@ -269,9 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Never leave with copies in flight.
         int zero = 0;
         for (uint32_t s = 0; s < S; ++s)
-          if (nk > s) ptx::mbar_wait(bar.kfull((int)s), ((nk - 1 - s) / S) & 1, &zero, a.err, kWaitLimit);
+          if (nk > s) wait_phase(bar.kfull((int)s), ((nk - 1 - s) / S) & 1, &zero, a.err);
         for (int x = 0; x < 2; ++x)
-          if (nq[x] > 0) ptx::mbar_wait(bar.qfull(x), (nq[x] - 1) & 1, &zero, a.err, kWaitLimit);
+          if (nq[x] > 0) wait_phase(bar.qfull(x), (nq[x] - 1) & 1, &zero, a.err);
       }
     } else if (warp == 13) {
       // ------------------------------------------------------------- the V ring
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (i == s) ph = land[i]++ & 1;
             // the copy is in flight: its landing is waited for even when the launch is given up
             int zero = 0;
-            const bool in = __all_sync(0xffffffffu, ptx::mbar_wait(bar.vland(s), ph, &zero, a.err, kWaitLimit));
+            const bool in = __all_sync(0xffffffffu, wait_phase(bar.vland(s), ph, &zero, a.err));
             if (!in) { *abort = 1; ok = false; break; }
             zero_masked_rows<D>(smem + C::kV + s * C::kTile, w, lane);
             if (lane == 0) ptx::mbar_arrive(bar.vfull(s));
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       int zero = 0;
       for (uint32_t s = 0; s < S; ++s)
-        if (nv > s) ptx::mbar_wait(bar.vfull((int)s), ((nv - 1 - s) / S) & 1, &zero, a.err, kWaitLimit);
+        if (nv > s) wait_phase(bar.vfull((int)s), ((nv - 1 - s) / S) & 1, &zero, a.err);
     } else if (warp == 14) {
       // ------------------------------------------------------------- MMA issuer
       // For each key tile, A and then B: P V of this tile, then the scores of the next (which
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Never free TMEM under a running product.
       int zero = 0;
       if (elect_one()) ptx::mma_commit(bar.drain());
-      ptx::mbar_wait(bar.drain(), 0, &zero, a.err, kWaitLimit);
+      wait_phase(bar.drain(), 0, &zero, a.err);
     }
   } else if (warp >= 8) {
     // --------------------------------------------------------------- output
