@@ -96,16 +96,18 @@ struct FwdArgs {
   float scale_log2;
 };
 
-// One unit: its item, key head, first token, and its range of key tiles.
+// One unit: its item, key head, first token, and its range of key tiles. Units follow one another
+// in the same object, so that an item's length is read once.
 struct Unit {
-  int b, hkv, n0, part, t0, t1, len;
-  __device__ __forceinline__ Unit(const FwdArgs& a, int u) {
+  int b = -1, hkv, n0, part, t0, t1, len;
+  __device__ __forceinline__ void open(const FwdArgs& a, int u) {
+    const int before = b;
     const int rest = (int)a.by_nqb.q((uint32_t)u), bh = (int)a.by_splits.q((uint32_t)rest);
     part = rest - bh * a.splits;
     b = (int)a.g.by_hkv.q((uint32_t)bh);
     hkv = bh - b * a.g.Hkv;
     n0 = (u - rest * a.nqb) * 2 * a.g.tpt;
-    len = item_keys(a.keys, b, a.g.M).x;
+    if (b != before) len = item_keys(a.keys, b, a.g.M).x;
     const int nt = (len + kCrossTile - 1) / kCrossTile;
     t0 = 0;
     t1 = nt;
@@ -149,12 +151,13 @@ __device__ __forceinline__ void exp32(const uint32_t* r, float c, float m, uint6
 // A key tile in the order in which the issuer meets them: the tiles of a unit, then the next unit
 // with any. `rows[x]` counts the units of block x so far, empty ones included.
 struct TileCursor {
+  Unit t;
   int u, kt, t0, t1;
   bool valid, has_b;
   uint32_t rows[2];
   __device__ __forceinline__ void open(const FwdArgs& a, int from) {
     for (u = from; u < a.units; u += gridDim.x) {
-      const Unit t(a, u);
+      t.open(a, u);
       has_b = t.n0 + a.g.tpt < a.g.N;
       ++rows[0];
       rows[1] += has_b;
@@ -228,8 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t nk = 0, nq[2] = {0, 0};
         bool ok = true;
         const uint32_t qbytes = (uint32_t)(g.G * g.tpt * D * 2);
+        Unit t, f;
         for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-          const Unit t(a, u);
+          t.open(a, u);
           auto load_q = [&](int x) {
             const int n = t.n0 + x * g.tpt;
             if (n >= g.N) return true;
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // The next unit's queries come from HBM meanwhile: their buffers are free only when
               // this unit's last scores are done.
               if (kt == t.t0 && u + (int)gridDim.x < a.units) {
-                const Unit f(a, u + (int)gridDim.x);
+                f.open(a, u + (int)gridDim.x);
                 for (int x = 0; x < 2; ++x)
                   if (f.t0 < f.t1 && f.n0 + x * g.tpt < g.N)
 #pragma unroll
@@ -281,8 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int s = 0; s < S; ++s) land[s] = 0;
       bool ok = true;
+      Unit t;
       for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-        const Unit t(a, u);
+        t.open(a, u);
         for (int kt = t.t0; kt < t.t1; ++kt) {
           const int s = (int)(nv % S);
           if (!warp_wait(bar.vempty(s), ((nv / S) & 1) ^ 1, abort, a.err)) { ok = false; break; }
@@ -386,8 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage = smem + C::kOut;
     uint32_t nl[2] = {0, 0}, no[2] = {0, 0};
     bool ok = true;
+    Unit t;
     for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-      const Unit t(a, u);
+      t.open(a, u);
       const bool any = t.t1 > t.t0;
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
@@ -455,11 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = a.scale_log2;
     uint32_t ns = 0, nu = 0;
     bool ok = true;
-    Unit ahead(a, (int)blockIdx.x < a.units ? blockIdx.x : 0);
+    Unit t;
     for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-      const Unit t = ahead;
-      const int after = u + (int)gridDim.x;
-      if (t.t0 == t.t1 || t.n0 + x * g.tpt >= g.N) ahead = Unit(a, after < a.units ? after : 0);
+      t.open(a, u);
       const int first = t.n0 + x * g.tpt;
       if (first >= g.N) continue;
       float m_run = -INFINITY, l = 0.f;
@@ -513,8 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar.pfull(x, h));
         }
-        // what the next unit is, under this one's products
-        if (kt == t.t0) ahead = Unit(a, after < a.units ? after : 0);
         float s0, s1;
         uf2(fadd2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
