@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -47,16 +48,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
                     "--expt-relaxed-constexpr", "-I", os.path.join(HERE, "..", "include")]
     if verbose:
         flags += ["-Xptxas", "-v"]
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(OBJDIR, src.replace(".cu", ".o"))
-        cmd = [cc, "-c", os.path.join(CSRC, src), "-o", obj] + flags
-        r = subprocess.run(cmd, capture_output=True, text=True)
+    objs = [os.path.join(OBJDIR, src.replace(".cu", ".o")) for src in SOURCES]
+    with ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        runs = list(pool.map(lambda so: subprocess.run([cc, "-c", os.path.join(CSRC, so[0]), "-o", so[1]] + flags,
+                                                       capture_output=True, text=True), zip(SOURCES, objs)))
+    for src, r in zip(SOURCES, runs):
         if r.returncode != 0 or verbose:
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}")
-        objs.append(obj)
     tmp = LIB + ".tmp"
     cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -17,13 +17,14 @@
 // to 256 elements takes 8, 16 or 32 lanes and a block several rows, and a longer row takes a
 // block of its own, with 2 or 4 slots a thread. Each thread copies its own slots of
 // the next three groups of rows to shared memory while one group is at work: the bytes in
-// flight cost no registers and no barrier. Rows whose width or address does not
-// allow 16-byte loads take the same kernels with single-element, coalesced loads.
+// flight cost no registers and no barrier. Rows of another even width go in pairs of elements, and odd widths (or
+// addresses that allow no more) in single coalesced loads without copies ahead.
 // The grid is persistent: each block takes one contiguous range of rows and in the backward pass
 // keeps the column sums of the rows it has seen. It writes them as one partial row for each item that its range meets; a second kernel adds
 // the partials of an item in the order of the blocks. No atomics: repeated calls give
 // identical bits.
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace bsa {
 namespace {
@@ -50,16 +51,14 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Column of element j of slot k of thread t: runs of E neighbouring elements a thread, E = 8 (16
-// bytes of bf16) or, where one side is fp32, 4 (16 bytes of that), or 1 where rows do not allow
-// wide accesses; neighbouring threads on neighbouring runs.
+// Column of element j of slot k of thread t: runs of E neighbouring elements a thread, neighbouring
+// threads on neighbouring runs. E = 8 (16 bytes of bf16) or, where one side is fp32, 4 (16 bytes
+// of that); 2 for rows of an even width that is not a multiple of 8; 1 for odd widths and
+// addresses that allow no more.
 template <int E>
 __device__ __forceinline__ int column(int t, int k, int j, int tpr) {
   return ((k * (8 / E) + j / E) * tpr + t) * E + j % E;
 }
-template <typename XT, typename YT, bool VEC>
-constexpr int kRun = !VEC ? 1 : sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
-
 // Eight elements of a row in registers: from global memory one by one, or (E > 1) from the runs
 // that the thread has copied to shared memory.
 template <typename T, int E>
@@ -77,17 +76,14 @@ struct Slot {
     }
   }
   __device__ __forceinline__ void take(const uint4* p, int plane) {
-    if (sizeof(T) == 2 && E == 4) {                 // two runs of 8 bytes in one 16-byte place
-      const uint2 a = reinterpret_cast<const uint2*>(p)[0], b = reinterpret_cast<const uint2*>(p)[1];
-      v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-    } else {
 #pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 u = p[i * plane];
-        v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
-      }
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 u = p[i * plane];
+      v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
     }
   }
+  // Elements 2 i and 2 i + 1.
+  __device__ __forceinline__ uint64_t pair(int i) const { return f2(get(2 * i), get(2 * i + 1)); }
   __device__ __forceinline__ float get(int j) const {
     if (sizeof(T) == 4) return __uint_as_float(v[j & (kWords - 1)]);
     return __uint_as_float((j & 1) ? (v[j >> 1] & 0xffff0000u) : (v[j >> 1] << 16));
@@ -105,14 +101,15 @@ __device__ __forceinline__ void copy_slot(uint4* dst, int plane, const T* row, i
   const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
 #pragma unroll
   for (int i = 0; i < 8 / E; ++i) {
-    const int c = column<E>(t, k, i * E, tpr);
+    const int c = column<E>(t, k, i * E, tpr), off = i * kBytes;
     const bool in = ok && c < C;
     const T* src = in ? row + c : row;
+    const uint32_t at = to + (uint32_t)((off >> 4) * 16 * plane + (off & 15));
     if (kBytes == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16 * i * plane), "l"(src), "r"(in ? 16 : 0)
-                   : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src), "r"(in ? 16 : 0) : "memory");
     else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + 8 * i), "l"(src), "r"(in ? 8 : 0) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(src), "n"(kBytes), "r"(in ? kBytes : 0)
+                   : "memory");
   }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -136,7 +133,8 @@ __device__ __forceinline__ void store_slot(T* row, int t, int k, int tpr, int C,
     const int c = column<E>(t, k, i * E, tpr);
     if (c >= C) continue;
     if (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(row + c) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      if (E == 2) *reinterpret_cast<float2*>(row + c) = make_float2(o[2 * i], o[2 * i + 1]);
+      else *reinterpret_cast<float4*>(row + c) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     } else {
       uint32_t u[4];
 #pragma unroll
@@ -145,7 +143,8 @@ __device__ __forceinline__ void store_slot(T* row, int t, int k, int tpr, int C,
         u[h] = *reinterpret_cast<const uint32_t*>(&p);
       }
       if (E == 8) *reinterpret_cast<uint4*>(row + c) = make_uint4(u[0], u[1], u[2], u[3]);
-      else *reinterpret_cast<uint2*>(row + c) = make_uint2(u[0], u[1]);
+      else if (E == 4) *reinterpret_cast<uint2*>(row + c) = make_uint2(u[0], u[1]);
+      else *reinterpret_cast<uint32_t*>(row + c) = u[0];
     }
   }
 }
@@ -154,16 +153,18 @@ __device__ __forceinline__ void store_slot(T* row, int t, int k, int tpr, int C,
 // item: read again for every group of rows they cost as much L2 traffic as the rows.
 template <int E>
 __device__ __forceinline__ void load_affine(const void* p, bool bf16, long long at, float add, float absent, int t,
-                                            int k, int tpr, int C, float (&o)[8]) {
+                                            int k, int tpr, int C, uint64_t (&o)[4]) {
+  float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int c = column<E>(t, k, j, tpr);
-    float v = absent;
+    v[j] = c < C ? absent : 0.f;
     if (p && c < C)
-      v = add + (bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + c])
-                      : static_cast<const float*>(p)[at + c]);
-    o[j] = c < C ? v : 0.f;
+      v[j] = add + (bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + c])
+                         : static_cast<const float*>(p)[at + c]);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = f2(v[2 * i], v[2 * i + 1]);
 }
 
 // Sums of S values over the threads of a row, left in every one of them. tpr <= 32: lanes of
@@ -192,7 +193,7 @@ __device__ __forceinline__ void row_sum(float (&s)[S], int tpr, float* red) {
 }
 
 // Rows are taken in groups of U a lane group; all but one of a ring of groups are on their way to
-// shared memory while one is at work (VEC). Four groups, fewer where T threads' pieces of them
+// shared memory while one is at work (E > 1). Four groups, fewer where T threads' pieces of them
 // are over 200 KB.
 template <typename XT, int VPT, int U>
 constexpr int kFwdPieces = U* VPT* kPieces<XT>;
@@ -203,11 +204,11 @@ constexpr int ring_depth(int pieces, int T) {
   return d < 1 ? 1 : d > 4 ? 4 : d;
 }
 
-template <typename XT, typename YT, bool VEC, int VPT, int U, int T, int kPerSm>
+template <typename XT, typename YT, int E, int VPT, int U, int T, int kPerSm>
 __global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
   __shared__ float red[2][U * 32];
   extern __shared__ uint4 ring[];         // [kDepth][piece][thread]
-  constexpr int E = kRun<XT, YT, VEC>;
+  constexpr bool kAhead = E > 1;
   constexpr int P = kPieces<XT>, kDepth = ring_depth(kFwdPieces<XT, VPT, U>, T);
   const int tpr = a.tpr, t = threadIdx.x % tpr, sub = threadIdx.x / tpr, rpb = blockDim.x / tpr, C = a.C;
   const int plane = blockDim.x;
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
   const long long step = (long long)rpb * U;
   for (long long r0 = lo; r0 < hi;) {
     const long long item = r0 / a.per, end = min(hi, (item + 1) * a.per), wat = a.w_items ? item * C : 0;
-    float w[VPT][8], b[VPT][8];
+    uint64_t w[VPT][4], b[VPT][4];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       load_affine<E>(a.w, a.w_bf16, wat, a.offset, 1.f, t, k, tpr, C, w[k]);
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
     }
     int put = 0, got = 0;                 // ring stages
     auto request = [&](long long base) {
-      if (VEC) {
+      if (kAhead) {
         uint4* dst = ring + put * (kFwdPieces<XT, VPT, U> * plane) + threadIdx.x;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
     for (long long base = r0; base < end; base += step) {
       Slot<XT, E> xs[U][VPT];
       request(base + (kDepth - 1) * step);
-      if constexpr (VEC) {
+      if constexpr (kAhead) {
         copies_wait<kDepth - 1>();
         const uint4* src = ring + got * (kFwdPieces<XT, VPT, U> * plane) + threadIdx.x;
 #pragma unroll
@@ -262,24 +263,38 @@ __global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
       float m[U], v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        m[u] = 0.f;
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m[u] += xs[u][k].get(j);
+          for (int i = 0; i < 4; ++i) sum[i & 1] = fadd2(sum[i & 1], xs[u][k].pair(i));
+        float s0, s1;
+        uf2(fadd2(sum[0], sum[1]), s0, s1);
+        m[u] = s0 + s1;
       }
       row_sum<U>(m, tpr, red[0]);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         m[u] *= inv_c;
-        v[u] = 0.f;
+        const uint64_t nm = f2(-m[u], -m[u]);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float d = xs[u][k].get(j) - m[u];
-            v[u] += column<E>(t, k, j, tpr) < C ? d * d : 0.f;
+          for (int i = 0; i < 4; ++i) {
+            uint64_t d = fadd2(xs[u][k].pair(i), nm);
+            if (E > 1) {
+              if (column<E>(t, k, 2 * i, tpr) >= C) d = 0ull;
+            } else {
+              float d0, d1;
+              uf2(d, d0, d1);
+              d = f2(column<E>(t, k, 2 * i, tpr) < C ? d0 : 0.f, column<E>(t, k, 2 * i + 1, tpr) < C ? d1 : 0.f);
+            }
+            sum[i & 1] = ffma2(d, d, sum[i & 1]);
           }
+        float s0, s1;
+        uf2(fadd2(sum[0], sum[1]), s0, s1);
+        v[u] = s0 + s1;
       }
       row_sum<U>(v, tpr, red[1]);
 #pragma unroll
@@ -296,9 +311,11 @@ __global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const long long r = base + u * rpb + sub;
+          const uint64_t nm = f2(-m[u], -m[u]), rs = f2(v[u], v[u]);
           float o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = (xs[u][k].get(j) - m[u]) * v[u] * w[k][j] + b[k][j];
+          for (int i = 0; i < 4; ++i)
+            uf2(ffma2(fmul2(fadd2(xs[u][k].pair(i), nm), rs), w[k][i], b[k][i]), o[2 * i], o[2 * i + 1]);
           if (r < end) store_slot<E>(y + r * C, t, k, tpr, C, o);
         }
       }
@@ -307,11 +324,11 @@ __global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
   }
 }
 
-template <typename XT, typename YT, bool VEC, int VPT, int U, int T, int kPerSm>
+template <typename XT, typename YT, int E, int VPT, int U, int T, int kPerSm>
 __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
   __shared__ float red[2][2 * U * 32];
   extern __shared__ uint4 ring[];         // [kDepth][piece][thread]
-  constexpr int E = kRun<XT, YT, VEC>;
+  constexpr bool kAhead = E > 1;
   constexpr int PX = kPieces<XT>, PY = kPieces<YT>, kDepth = ring_depth(kBwdPieces<XT, YT, VPT, U>, T);
   const int tpr = a.tpr, t = threadIdx.x % tpr, sub = threadIdx.x / tpr, rpb = blockDim.x / tpr, C = a.C;
   const int plane = blockDim.x;
@@ -320,22 +337,22 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
   const YT* dy = static_cast<const YT*>(a.dy);
   XT* dx = static_cast<XT*>(a.y);
   // several rows a block: their column sums [2][C] meet here, behind the ring
-  float* acc = reinterpret_cast<float*>(ring + (VEC ? kDepth * kBwdPieces<XT, YT, VPT, U> * plane : 0));
+  float* acc = reinterpret_cast<float*>(ring + (kAhead ? kDepth * kBwdPieces<XT, YT, VPT, U> * plane : 0));
   const long long lo = a.rows * blockIdx.x / gridDim.x, hi = a.rows * (blockIdx.x + 1) / gridDim.x;
   const long long step = (long long)rpb * U;
   int flip = 0;
   for (long long r0 = lo; r0 < hi;) {
     const long long item = r0 / a.per, end = min(hi, (item + 1) * a.per), wat = a.w_items ? item * C : 0;
-    float w[VPT][8], dw[VPT][8], db[VPT][8];
+    uint64_t w[VPT][4], dw[VPT][4], db[VPT][4];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) load_affine<E>(a.w, a.w_bf16, wat, a.offset, 1.f, t, k, tpr, C, w[k]);
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.f;
+      for (int i = 0; i < 4; ++i) dw[k][i] = db[k][i] = 0ull;
     int put = 0, got = 0;                 // ring stages
     auto request = [&](long long base) {
-      if (VEC) {
+      if (kAhead) {
         uint4* dst = ring + put * (kBwdPieces<XT, YT, VPT, U> * plane) + threadIdx.x;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -359,11 +376,11 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const long long r = base + u * rpb + sub, q = r < end ? r : base;
-        m[u] = a.mean[q];
-        rs[u] = a.rstd[q];
-        s[2 * u] = s[2 * u + 1] = 0.f;
+        // a row that is not there: dy is zero, and so is h, whatever another row's statistics are
+        m[u] = r < end ? a.mean[q] : 0.f;
+        rs[u] = r < end ? a.rstd[q] : 0.f;
       }
-      if constexpr (VEC) {
+      if constexpr (kAhead) {
         copies_wait<kDepth - 1>();
         const uint4* src = ring + got * (kBwdPieces<XT, YT, VPT, U> * plane) + threadIdx.x;
 #pragma unroll
@@ -385,21 +402,31 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
           }
         }
       }
+      uint64_t s1[U], s2[U];
 #pragma unroll
-      for (int k = 0; k < VPT; ++k) {
+      for (int u = 0; u < U; ++u) s1[u] = s2[u] = 0ull;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const bool in = base + u * rpb + sub < end;
+          const uint64_t nm = f2(-m[u], -m[u]), r2 = f2(rs[u], rs[u]);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int i = 0; i < 4; ++i) {
             // past the row's end dy is zero, so none of the sums sees the element
-            const float d = gs[u][k].get(j), h = (xs[u][k].get(j) - m[u]) * rs[u], g = d * w[k][j];
-            s[2 * u] += g;
-            s[2 * u + 1] += g * h;
-            dw[k][j] += in ? d * h : 0.f;
-            db[k][j] += d;
+            const uint64_t d = gs[u][k].pair(i), h = fmul2(fadd2(xs[u][k].pair(i), nm), r2), g = fmul2(d, w[k][i]);
+            s1[u] = fadd2(s1[u], g);
+            s2[u] = ffma2(g, h, s2[u]);
+            dw[k][i] = ffma2(d, h, dw[k][i]);
+            db[k][i] = fadd2(db[k][i], d);
           }
         }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float p0, p1;
+        uf2(s1[u], p0, p1);
+        s[2 * u] = p0 + p1;
+        uf2(s2[u], p0, p1);
+        s[2 * u + 1] = p0 + p1;
       }
       row_sum<2 * U>(s, tpr, red[flip]);
       flip ^= 1;
@@ -409,11 +436,12 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
         for (int u = 0; u < U; ++u) {
           const long long r = base + u * rpb + sub;
           const float c1 = s[2 * u] * inv_c, c2 = s[2 * u + 1] * inv_c;
+          const uint64_t nm = f2(-m[u], -m[u]), r2 = f2(rs[u], rs[u]), n1 = f2(-c1, -c1), n2 = f2(-c2, -c2);
           float o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float h = (xs[u][k].get(j) - m[u]) * rs[u];
-            o[j] = rs[u] * (gs[u][k].get(j) * w[k][j] - c1 - h * c2);
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t h = fmul2(fadd2(xs[u][k].pair(i), nm), r2);
+            uf2(fmul2(ffma2(h, n2, ffma2(gs[u][k].pair(i), w[k][i], n1)), r2), o[2 * i], o[2 * i + 1]);
           }
           if (r < end) store_slot<E>(dx + r * C, t, k, tpr, C, o);
         }
@@ -424,13 +452,21 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
       // so no two (block, item) pairs share it
       float* pw = a.part + (blockIdx.x + (a.w_items ? item : 0)) * C;
       float* pb = pw + a.slots * C;
+      float vw[VPT][8], vb[VPT][8];
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uf2(dw[k][i], vw[k][2 * i], vw[k][2 * i + 1]);
+          uf2(db[k][i], vb[k][2 * i], vb[k][2 * i + 1]);
+        }
       if (rpb == 1) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int c = column<E>(t, k, j, tpr);
-            if (c < C) pw[c] = dw[k][j], pb[c] = db[k][j];
+            if (c < C) pw[c] = vw[k][j], pb[c] = vb[k][j];
           }
       } else {
         for (int g = 0; g < rpb; ++g) {     // the rows' sums one after the other, in a fixed order
@@ -441,8 +477,8 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
               for (int j = 0; j < 8; ++j) {
                 const int c = column<E>(t, k, j, tpr);
                 if (c < C) {
-                  acc[c] = g == 0 ? dw[k][j] : acc[c] + dw[k][j];
-                  acc[C + c] = g == 0 ? db[k][j] : acc[C + c] + db[k][j];
+                  acc[c] = g == 0 ? vw[k][j] : acc[c] + vw[k][j];
+                  acc[C + c] = g == 0 ? vb[k][j] : acc[C + c] + vb[k][j];
                 }
               }
           __syncthreads();
@@ -493,8 +529,8 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
 struct NormShape {
   int tpr, vpt, threads;
 };
-NormShape norm_shape(int C, bool bwd, bool fp32, bool vec) {
-  const int slots = ceil_div(C, 8), most = !vec ? 1 : bwd || fp32 ? 2 : 4;
+NormShape norm_shape(int C, bool bwd, bool fp32, int run) {
+  const int slots = ceil_div(C, 8), most = run == 1 ? 1 : bwd || fp32 || run == 2 ? 2 : 4;
   NormShape n;
   if (slots <= 32 * most) {                         // a warp or less
     n.vpt = slots <= 32 ? 1 : slots <= 64 ? 2 : 4;
@@ -502,7 +538,7 @@ NormShape norm_shape(int C, bool bwd, bool fp32, bool vec) {
     n.threads = 256;
     return n;
   }
-  if (!vec) {                                       // no copies ahead: as many threads as go
+  if (run == 1) {                                    // no copies ahead: as many threads as go
     n.vpt = slots <= 640 ? 1 : slots <= 1024 ? 2 : 4;
   } else {                                          // the fewest lanes without work, then the fewest threads
     n.vpt = most == 4 && 128 * ceil_div(slots, 128) <= 64 * ceil_div(slots, 64) ? 4 : 2;
@@ -515,22 +551,22 @@ NormShape norm_shape(int C, bool bwd, bool fp32, bool vec) {
 constexpr int kNormSms = 148;     // SMs of the part; the workspace is sized without asking the device
 
 // Rows that a lane group takes together: more make fewer reductions, fewer leave registers.
-template <typename XT, bool VEC, int VPT>
-constexpr int kFwdU = !VEC ? 1 : VPT == 1 ? 8 / sizeof(XT) : VPT == 2 ? 4 / sizeof(XT) : 1;
-template <bool VEC, int VPT>
-constexpr int kBwdU = VEC && VPT == 1 ? 2 : 1;
+template <typename XT, int E, int VPT>
+constexpr int kFwdU = E == 1 ? 1 : VPT == 1 ? 8 / sizeof(XT) : VPT == 2 ? 4 / sizeof(XT) : 1;
+template <int E, int VPT>
+constexpr int kBwdU = E > 1 && VPT == 1 ? 2 : 1;
 
 // Blocks an SM that a kernel is built for: registers to hold everything (what does not fit goes
 // through L2, since the copies ahead leave L1 little: a backward pass with 216 bytes of it a
 // thread took twice as long).
-constexpr int per_sm(int vpt, int T) { return T > 256 ? 1 : vpt == 1 ? 3 : 2; }
+constexpr int per_sm(int vpt, int T, bool bwd) { return T > 256 ? 1 : vpt == 1 && !bwd ? 3 : 2; }
 
 // Blocks of a launch: enough to fill the device, never more than there are rows for one each of a
 // block's lane groups.
-int norm_blocks(const NormShape& n, long long rows) {
+int norm_blocks(const NormShape& n, long long rows, bool bwd) {
   const long long step = n.threads / n.tpr, need = (rows + step - 1) / step;
   const int T = n.threads > 256 ? n.threads : 256;
-  const long long full = (long long)kNormSms * (per_sm(n.vpt, T) * T / n.threads);
+  const long long full = (long long)kNormSms * (per_sm(n.vpt, T, bwd) * T / n.threads);
   return (int)(need < full ? need : full);
 }
 
@@ -549,38 +585,36 @@ cudaError_t start(const NormArgs& a, int blocks, int threads, size_t smem, size_
   return cudaGetLastError();
 }
 
-template <typename XT, typename YT, bool VEC, int VPT, int T>
+template <typename XT, typename YT, int E, int VPT, int T>
 cudaError_t run_fwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
-  constexpr int U = kFwdU<XT, VEC, VPT>, kPieces = kFwdPieces<XT, VPT, U>;
-  constexpr size_t kThread = VEC ? 16 * ring_depth(kPieces, T) * kPieces : 0;
-  return start<norm_fwd_kernel<XT, YT, VEC, VPT, U, T, per_sm(VPT, T)>>(a, blocks, n.threads, kThread * n.threads,
+  constexpr int U = kFwdU<XT, E, VPT>, kPieces = kFwdPieces<XT, VPT, U>;
+  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T) * kPieces : 0;
+  return start<norm_fwd_kernel<XT, YT, E, VPT, U, T, per_sm(VPT, T, false)>>(a, blocks, n.threads, kThread * n.threads,
                                                                         kThread * T, s);
 }
-template <typename XT, typename YT, bool VEC, int VPT, int T>
+template <typename XT, typename YT, int E, int VPT, int T>
 cudaError_t run_bwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
-  constexpr int U = kBwdU<VEC, VPT>, kPieces = kBwdPieces<XT, YT, VPT, U>;
-  constexpr size_t kThread = VEC ? 16 * ring_depth(kPieces, T) * kPieces : 0;
+  constexpr int U = kBwdU<E, VPT>, kPieces = kBwdPieces<XT, YT, VPT, U>;
+  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T) * kPieces : 0;
   const size_t acc = n.tpr < n.threads && a.part ? 2 * sizeof(float) * a.C : 0;      // rows of at most 512
-  return start<norm_bwd_kernel<XT, YT, VEC, VPT, U, T, per_sm(VPT, T)>>(
+  return start<norm_bwd_kernel<XT, YT, E, VPT, U, T, per_sm(VPT, T, true)>>(
       a, blocks, n.threads, kThread * n.threads + acc, kThread * T + 2 * sizeof(float) * 512, s);
 }
 
-template <typename XT, typename YT, bool VEC, int VPT, int T>
+template <typename XT, typename YT, int E, int VPT, int T>
 cudaError_t run_either(const NormArgs& a, bool bwd, const NormShape& n, int blocks, cudaStream_t s) {
-  return bwd ? run_bwd<XT, YT, VEC, VPT, T>(a, n, blocks, s) : run_fwd<XT, YT, VEC, VPT, T>(a, n, blocks, s);
+  return bwd ? run_bwd<XT, YT, E, VPT, T>(a, n, blocks, s) : run_fwd<XT, YT, E, VPT, T>(a, n, blocks, s);
 }
-template <typename XT, typename YT, bool VEC>
+template <typename XT, typename YT, int E>
 cudaError_t run_norm(const NormArgs& a, bool bwd, const NormShape& n, int blocks, cudaStream_t s) {
   const bool wide = n.threads > 256;
-  if (n.vpt == 1 && wide) return run_either<XT, YT, false, 1, 640>(a, bwd, n, blocks, s);   // rows without wide accesses only
-  if (n.vpt == 1) return run_either<XT, YT, VEC, 1, 256>(a, bwd, n, blocks, s);
-  if (n.vpt == 2 && wide) return run_either<XT, YT, VEC, 2, 512>(a, bwd, n, blocks, s);
-  if (n.vpt == 2) return run_either<XT, YT, VEC, 2, 256>(a, bwd, n, blocks, s);
-  if (wide) return run_either<XT, YT, VEC, 4, 512>(a, bwd, n, blocks, s);
-  return run_fwd<XT, YT, VEC, 4, 256>(a, n, blocks, s);       // the backward pass has 4 slots only past 256 threads
+  if (n.vpt == 1 && wide) return run_either<XT, YT, 1, 1, 640>(a, bwd, n, blocks, s);   // E = 1 only
+  if (n.vpt == 1) return run_either<XT, YT, E, 1, 256>(a, bwd, n, blocks, s);
+  if (n.vpt == 2 && wide) return run_either<XT, YT, E, 2, 512>(a, bwd, n, blocks, s);
+  if (n.vpt == 2) return run_either<XT, YT, E, 2, 256>(a, bwd, n, blocks, s);
+  if (wide) return run_either<XT, YT, E, 4, 512>(a, bwd, n, blocks, s);
+  return run_fwd<XT, YT, E, 4, 256>(a, n, blocks, s);       // the backward pass has 4 slots only past 256 threads
 }
-
-bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 NormArgs norm_args(const bsa_norm_shape& f) {
   NormArgs a = {};
@@ -594,26 +628,42 @@ NormArgs norm_args(const bsa_norm_shape& f) {
   return a;
 }
 
+template <typename XT, typename YT>
+cudaError_t run_any(const NormArgs& a, int run, bool bwd, const NormShape& n, int blocks, cudaStream_t s) {
+  constexpr int kWide = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
+  if (run == 2) return run_norm<XT, YT, 2>(a, bwd, n, blocks, s);
+  return run == 1 ? run_norm<XT, YT, 1>(a, bwd, n, blocks, s) : run_norm<XT, YT, kWide>(a, bwd, n, blocks, s);
+}
+
 cudaError_t dispatch(const bsa_norm_shape& f, NormArgs& a, bool bwd, cudaStream_t s, int* blocks_out = nullptr) {
-  const bool vec = f.C % 8 == 0 && at16(a.x) && at16(a.y) && at16(a.dy);
-  const NormShape n = norm_shape(f.C, bwd, f.x_type == BSA_FP32, vec);
-  const int blocks = norm_blocks(n, f.rows);
+  const bool xb = f.x_type == BSA_BF16, yb = f.y_type == BSA_BF16;
+  // x, and in the backward pass dx, are of one type, y or dy of the other; all rows start alike
+  // where the width is a multiple of the run
+  auto allows = [&](int run) {
+    auto at = [run](const void* p, bool bf16) {
+      const uintptr_t bytes = (uintptr_t)run * (bf16 ? 2 : 4);
+      return (reinterpret_cast<uintptr_t>(p) & ((bytes < 16 ? bytes : 16) - 1)) == 0;
+    };
+    return f.C % run == 0 && at(a.x, xb) && at(a.y, bwd ? xb : yb) && at(a.dy, yb);
+  };
+  const int run = allows(8) ? 8 : allows(2) ? 2 : 1;
+  const NormShape n = norm_shape(f.C, bwd, !xb, run);
+  const int blocks = norm_blocks(n, f.rows, bwd);
   a.tpr = n.tpr;
   a.slots = blocks + (a.w_items ? f.items : 1);
   if (blocks_out) *blocks_out = blocks;
-  const bool xb = f.x_type == BSA_BF16, yb = f.y_type == BSA_BF16;
-  if (xb && yb) return vec ? run_norm<__nv_bfloat16, __nv_bfloat16, true>(a, bwd, n, blocks, s) : run_norm<__nv_bfloat16, __nv_bfloat16, false>(a, bwd, n, blocks, s);
-  if (xb) return vec ? run_norm<__nv_bfloat16, float, true>(a, bwd, n, blocks, s) : run_norm<__nv_bfloat16, float, false>(a, bwd, n, blocks, s);
-  if (yb) return vec ? run_norm<float, __nv_bfloat16, true>(a, bwd, n, blocks, s) : run_norm<float, __nv_bfloat16, false>(a, bwd, n, blocks, s);
-  return vec ? run_norm<float, float, true>(a, bwd, n, blocks, s) : run_norm<float, float, false>(a, bwd, n, blocks, s);
+  if (xb && yb) return run_any<__nv_bfloat16, __nv_bfloat16>(a, run, bwd, n, blocks, s);
+  if (xb) return run_any<__nv_bfloat16, float>(a, run, bwd, n, blocks, s);
+  if (yb) return run_any<float, __nv_bfloat16>(a, run, bwd, n, blocks, s);
+  return run_any<float, float>(a, run, bwd, n, blocks, s);
 }
 
 }  // namespace
 
 size_t norm_workspace(const bsa_norm_shape& f) {
   int blocks = 0;                 // whatever the addresses allow
-  for (const bool vec : {false, true}) {
-    const int n = norm_blocks(norm_shape(f.C, true, f.x_type == BSA_FP32, vec), f.rows);
+  for (const int run : {1, 2, 8}) {
+    const int n = norm_blocks(norm_shape(f.C, true, f.x_type == BSA_FP32, run), f.rows, true);
     if (n > blocks) blocks = n;
   }
   return align256((size_t)(blocks + (f.w_per_item ? f.items : 1)) * f.C * 2 * sizeof(float));

@@ -98,7 +98,9 @@ def check(shape, xt=BF, yt=BF, affine="shared", seed=0, wt=F32, eps=1e-6, off=0.
 
 
 SHAPES = [(1, 1536), (1, 1), (3, 7), (5, 64), (33, 128), (2, 9, 12, 128), (17, 200), (9, 257), (40, 256), (11, 1001),
-          (6, 5120), (3, 5128), (5, 5121), (2, 10240), (2, 10248), (3, 16384), (2, 16383), (700, 96), (1500, 520)]
+          (6, 5120), (3, 5128), (5, 5121), (2, 10240), (2, 10248), (3, 16384), (2, 16383), (700, 96), (1500, 520),
+          # even widths that are not multiples of 8: below a warp, one and two slots a thread, and wide
+          (33, 10), (40, 250), (12, 258), (9, 514), (7, 1002), (5, 4098), (3, 5446), (3, 9002), (2, 16382)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
