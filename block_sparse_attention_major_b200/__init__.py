@@ -487,6 +487,28 @@ def sparse_attn_fwd_fixed_scratch(g: Geometry, qt: torch.Tensor, kt: torch.Tenso
     return out, lse
 
 
+def _owned_by(stream):
+    """Allocations inside belong to `stream` (the current one if None): memory that only the
+    call's own stream touches may then be freed, and reused there, as soon as the call returns."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """An output of a call on `stream`, whose memory belongs to it (see _owned_by)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _given(t: torch.Tensor | None, like: torch.Tensor, dtype, shape, name: str, stream) -> torch.Tensor:
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        return _new(like, shape, dtype, stream)
+    _need(t, dtype, shape, name)
+    return t
+
+
 def cross_workspace_bytes(g: CrossGeometry) -> int:
     return int(load_library().bsa_cross_workspace_bytes(ctypes.byref(g.c())))
 
@@ -526,6 +548,14 @@ def _cross_inputs(g: CrossGeometry, q, k, v, kv_len, key_mask):
     return ctypes.byref(bsa_cross_strides(*(three(*t.stride()[:3]) for t in (q, k, v))))
 
 
+def _cross_ws(g: CrossGeometry, ws, like: torch.Tensor, stream) -> torch.Tensor:
+    if ws is None:
+        with _owned_by(stream):
+            return alloc_cross_workspace(g, like.device)
+    _need_ws(ws)
+    return ws
+
+
 def cross_attn_fwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                    kv_len: torch.Tensor | None = None, key_mask: torch.Tensor | None = None,
                    scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
@@ -537,18 +567,10 @@ def cross_attn_fwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.
     kv_len (int32 [B]) and key_mask (bool [B,M]) say which keys of an item are valid; an item
     without one gives 0 and an lse of -inf. Returns (out bf16 [B,N,H,d], lse fp32 [B,H,N])."""
     st = _cross_inputs(g, q, k, v, kv_len, key_mask)
-    dev = q.device
-    with _owned_by(stream):
-        if out is None:
-            out = q.new_empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16)
-        if want_lse and lse is None:
-            lse = q.new_empty((g.B, g.H, g.N), dtype=torch.float32)
-        if ws is None:
-            ws = alloc_cross_workspace(g, dev)
-    _need(out, torch.bfloat16, (g.B, g.N, g.H, g.d), "out")
-    if lse is not None:
-        _need(lse, torch.float32, (g.B, g.H, g.N), "lse")
-    _need_ws(ws)
+    out = _given(out, q, torch.bfloat16, (g.B, g.N, g.H, g.d), "out", stream)
+    if want_lse or lse is not None:
+        lse = _given(lse, q, torch.float32, (g.B, g.H, g.N), "lse", stream)
+    ws = _cross_ws(g, ws, q, stream)
     sc = 1.0 / math.sqrt(g.d) if scale is None else float(scale)
     _call("bsa_cross_attn_fwd", (q, k, v, kv_len, key_mask, out, lse, ws), stream, load_library().bsa_cross_attn_fwd,
           _cross_geom_ref(g), st, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(kv_len), _addr(key_mask), sc,
@@ -568,20 +590,10 @@ def cross_attn_bwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.
     _need(out, torch.bfloat16, (g.B, g.N, g.H, g.d), "out")
     _need(dout, torch.bfloat16, (g.B, g.N, g.H, g.d), "dout")
     _need(lse, torch.float32, (g.B, g.H, g.N), "lse")
-    dev = q.device
-    with _owned_by(stream):
-        if dq is None:
-            dq = q.new_empty((g.B, g.N, g.H, g.d), dtype=torch.bfloat16)
-        if dk is None:
-            dk = q.new_empty((g.B, g.M, g.Hkv, g.d), dtype=torch.bfloat16)
-        if dv is None:
-            dv = q.new_empty((g.B, g.M, g.Hkv, g.d), dtype=torch.bfloat16)
-        if ws is None:
-            ws = alloc_cross_workspace(g, dev)
-    _need(dq, torch.bfloat16, (g.B, g.N, g.H, g.d), "dq")
-    _need(dk, torch.bfloat16, (g.B, g.M, g.Hkv, g.d), "dk")
-    _need(dv, torch.bfloat16, (g.B, g.M, g.Hkv, g.d), "dv")
-    _need_ws(ws)
+    dq = _given(dq, q, torch.bfloat16, (g.B, g.N, g.H, g.d), "dq", stream)
+    dk = _given(dk, q, torch.bfloat16, (g.B, g.M, g.Hkv, g.d), "dk", stream)
+    dv = _given(dv, q, torch.bfloat16, (g.B, g.M, g.Hkv, g.d), "dv", stream)
+    ws = _cross_ws(g, ws, q, stream)
     sc = 1.0 / math.sqrt(g.d) if scale is None else float(scale)
     _call("bsa_cross_attn_bwd", (q, k, v, out, lse, dout, kv_len, key_mask, dq, dk, dv, ws), stream,
           load_library().bsa_cross_attn_bwd, _cross_geom_ref(g), st, q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -593,7 +605,10 @@ def cross_attn_bwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.
 def _call(what: str, tensors, stream, fn, *args) -> None:
     """fn(*args, stream handle) on the one device of `tensors`, made current if it is not: _run for
     the calls whose few microseconds of marshalling count."""
-    dev = _device_of(*tensors)
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            _device_of(*tensors)
     if stream is None and dev.type == "cuda":
         handle = torch._C._cuda_getCurrentRawStream(dev.index)    # without the Stream object, 2 us
     else:
@@ -615,12 +630,6 @@ def _cross_geom_ref(g: CrossGeometry):
 
 
 _NORM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
-
-
-def _owned_by(stream):
-    """Allocations inside belong to `stream` (the current one if None): memory that only the
-    call's own stream touches may then be freed, and reused there, as soon as the call returns."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 @functools.lru_cache(maxsize=256)
@@ -667,17 +676,11 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     the backward pass (None without want_stats)."""
     dt = y.dtype if y is not None and out_dtype is None else out_dtype or getattr(x, "dtype", None)
     f = _norm_shape(x, dt, weight, bias, eps, weight_offset)
-    with _owned_by(stream):
-        if y is None:
-            y = x.new_empty(x.shape, dtype=dt)
-        if want_stats and mean is None:
-            mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
-        if want_stats and rstd is None:
-            rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    _need(y, dt, x.shape, "y")
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None:
-            _need(t, torch.float32, x.shape[:-1], name)
+    y = _given(y, x, dt, x.shape, "y", stream)
+    if want_stats or mean is not None:
+        mean = _given(mean, x, torch.float32, x.shape[:-1], "mean", stream)
+    if want_stats or rstd is not None:
+        rstd = _given(rstd, x, torch.float32, x.shape[:-1], "rstd", stream)
     _call("bsa_layer_norm_fwd", (x, weight, bias, y, mean, rstd), stream, load_library().bsa_layer_norm_fwd,
           ctypes.byref(f), x.data_ptr(), _addr(weight), _addr(bias), y.data_ptr(), _addr(mean), _addr(rstd))
     return y, mean, rstd
@@ -711,21 +714,16 @@ def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: 
         raise ValueError("dweight and dbias need the weight")
     want_weight = weight is not None and (want_weight or dweight is not None)
     want_bias = weight is not None and (want_bias or dbias is not None)
-    with _owned_by(stream):
-        if dx is None:
-            dx = x.new_empty(x.shape, dtype=x.dtype)
-        if want_weight and dweight is None:
-            dweight = x.new_empty(weight.shape, dtype=torch.float32)
-        if want_bias and dbias is None:
-            dbias = x.new_empty(weight.shape, dtype=torch.float32)
-        if ws is None and (want_weight or want_bias):
-            ws = alloc_layer_norm_workspace(x, weight)
-    _need(dx, x.dtype, x.shape, "dx")
-    for name, t in (("dweight", dweight), ("dbias", dbias)):
-        if t is not None:
-            _need(t, torch.float32, weight.shape, name)
+    dx = _given(dx, x, x.dtype, x.shape, "dx", stream)
+    if want_weight:
+        dweight = _given(dweight, x, torch.float32, weight.shape, "dweight", stream)
+    if want_bias:
+        dbias = _given(dbias, x, torch.float32, weight.shape, "dbias", stream)
     if ws is not None:
         _need_ws(ws)
+    elif want_weight or want_bias:
+        with _owned_by(stream):
+            ws = alloc_layer_norm_workspace(x, weight)
     _call("bsa_layer_norm_bwd", (x, dy, mean, rstd, weight, dx, dweight, dbias, ws), stream,
           load_library().bsa_layer_norm_bwd, ctypes.byref(f), x.data_ptr(), dy.data_ptr(), mean.data_ptr(),
           rstd.data_ptr(), _addr(weight), dx.data_ptr(), _addr(dweight), _addr(dbias), _addr(ws),

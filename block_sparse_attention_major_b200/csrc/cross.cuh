@@ -72,12 +72,15 @@ struct CrossWs {
   size_t plan, bits, prefix, stats, part, total;
 };
 
-// Parts that the keys are split into when the query tiles alone do not fill the device.
+// Parts that the keys are split into when the query tiles alone do not fill the device. Joining
+// takes a launch and some 3 us, so short walks stay whole (one query and 12 heads over 512 keys:
+// 11.0 us, in 4 parts 6.3 + 3.0 us and the launch), and a part has at least two tiles (1024 keys:
+// 11.1 us in parts of 4 tiles, 7.1 us in parts of 1, the join 2.9 and 4.1 us).
 inline int cross_splits(const CrossGeom& g) {
   const long long units = (long long)g.B * g.Hkv * ceil_div(g.nqt, 2);
-  if (units * 2 > kCrossSms) return 1;
-  const long long s = kCrossSms / units;
-  return (int)(s < g.nkt ? s : g.nkt);
+  if (units * 2 > kCrossSms || g.nkt < 8) return 1;
+  const long long s = kCrossSms / units, most = g.nkt / 2;
+  return (int)(s < most ? s : most);
 }
 
 inline CrossWs cross_ws(const CrossGeom& g) {
