@@ -5,7 +5,8 @@
 //   ds_ij = p_ij (t_ij - D_i)
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
 //
-// Three kernels. The row statistics (lse in units of log 2, D) are computed once. Then one kernel
+// Three kernels. The row statistics (lse in units of log 2, D) are computed once (D again where one
+// key tile holds a row). Then one kernel
 // keeps 128 query rows and walks the keys (dq), and one keeps 128 keys and walks the query rows
 // (dk, dv), each computing the scores and t again: seven products where one kernel would need
 // five, but no sum crosses a CTA on the way, so there are no atomics, and repeated calls give
@@ -37,7 +38,7 @@ constexpr int kThreads = 384;
 struct BwdArgs {
   CrossGeom g;
   KeySet keys;
-  const float2* stats;              // [B, H, N]: (lse / log 2, D); +inf for a row without a key
+  float2* stats;                    // [B, H, N]: (lse / log 2, D); +inf for a row without a key
   const int* prefix;                // key tiles of the items before b; null: every item has nkt
   int kb_mul, vb_mul, qb_mul;
   __nv_bfloat16 *dk, *dv;
@@ -51,13 +52,17 @@ __device__ __forceinline__ int key_tiles(const BwdArgs& a, int b) {
   return (item_keys(a.keys, b, a.g.M).x + kCrossTile - 1) / kCrossTile;
 }
 
-// (lse, D) of the row r of query tile qt of (b, hkv); rows past the tokens or the tile's heads
-// take +inf: their probabilities are zero.
-__device__ __forceinline__ float2 row_stats(const BwdArgs& a, int b, int hkv, int qt, int r) {
+// Place of (lse, D) of row r of query tile qt of (b, hkv), or -1 for rows past the tokens or the tile's
+// heads, which take lse = +inf: their probabilities are zero.
+__device__ __forceinline__ long long stats_at(const BwdArgs& a, int b, int hkv, int qt, int r) {
   const CrossGeom& g = a.g;
   const int rt = (int)g.by_G.q((uint32_t)r), tok = qt * g.tpt + rt, head = hkv * g.G + r - rt * g.G;
-  if (r >= g.G * g.tpt || tok >= g.N) return make_float2(INFINITY, 0.f);
-  return a.stats[((long long)b * g.H + head) * g.N + tok];
+  if (r >= g.G * g.tpt || tok >= g.N) return -1;
+  return ((long long)b * g.H + head) * g.N + tok;
+}
+__device__ __forceinline__ float2 row_stats(const BwdArgs& a, int b, int hkv, int qt, int r) {
+  const long long i = stats_at(a, b, hkv, qt, r);
+  return i < 0 ? make_float2(INFINITY, 0.f) : a.stats[i];
 }
 
 // -------------------------------------------------------------------------------- dq
@@ -68,7 +73,8 @@ struct CfgQ {
   static constexpr int kKS = 3, kVS = D == 128 ? 1 : 2;
   static constexpr int kQ = 0, kDo = kTile, kK = 2 * kTile, kV = kK + kKS * kTile;
   static constexpr int kOut = kV + kVS * kTile;             // staging of a finished block
-  static constexpr int kBar = kOut + kTile;
+  static constexpr int kSum = kOut + kTile;                 // [2][128] sums of half rows
+  static constexpr int kBar = kSum + 2 * kCrossTile * 4;
   // kfull, kempty, kland [kKS]; vfull, vempty [kVS]; sfull [2]; qfull, qempty, dofull, doempty, tfull, dsfull,
   // done, drain
   static constexpr int kBars = 3 * kKS + 2 * kVS + 2 + 8;
@@ -342,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const float2 st = row_stats(a, b, hkv, qt, row);
-      const uint64_t cc = f2(c, c), mm = f2(-st.x, -st.x), dd = f2(-st.y, -st.y);
+      const uint64_t cc = f2(c, c), mm = f2(-st.x, -st.x);
+      uint64_t dd = f2(-st.y, -st.y);
       for (int i = 0; i < nt; ++i, ++n) {
         const uint4 w4 = tile_bits(a.keys, b, i, g.nkt, ik.x);
         const bool full = all_set(w4);
@@ -367,7 +374,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           held = -1;
           if (!ok) break;
         }
-        if (!warp_wait(tfull, n & 1, abort, a.err)) { ok = false; break; }
+        ok = warp_wait(tfull, n & 1, abort, a.err);
+        if (nt == 1) {
+          // The whole row is here: D = sum_j p t, instead of the sum over the rounded output, whose
+          // error is the larger against dS the fewer keys share a row. The two halves of a row
+          // meet in shared memory; the dk, dv kernel reads the same D.
+          float* s_sum = reinterpret_cast<float*>(smem + C::kSum);
+          if (ok) {
+            ptx::tc_fence_after();
+            float sum = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t t[32];
+              tmem_ld_x32(t_tmem + 32 * h, t);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                sum += ((w[h] >> k) & 1u) ? __uint_as_float(t[k]) * __uint_as_float(p[32 * h + k]) : 0.f;
+            }
+            s_sum[half * kCrossTile + row] = sum;
+          }
+          ok = bar_all(1, 256, ok);
+          if (ok) {
+            const float sum = s_sum[row] + s_sum[kCrossTile + row];
+            dd = f2(-sum, -sum);
+            const long long at = stats_at(a, b, hkv, qt, row);
+            if (half == 0 && at >= 0) a.stats[at].y = sum;
+          }
+        }
+        if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

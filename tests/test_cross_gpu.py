@@ -213,6 +213,24 @@ def test_one_valid_key():
     assert not dq.any() and not dk.any()
 
 
+@pytest.mark.parametrize("M", [2, 3, 5, 17, 128])
+def test_gradients_of_few_keys_keep_two_roundings(M):
+    # dq and dk carry the rounding of dS and that of the result, each uniform within R of the value at
+    # most: R / sqrt(3) each, sqrt(2 / 3) R together. D taken from the rounded output would add as
+    # much again where few keys share a row.
+    import block_sparse_attention_major_b200 as bsa
+    B, N, H, d = 2, 700, 4, 128
+    g = bsa.CrossGeometry(B, H, H, d, N, M)
+    q, k, v, do = randn((B, N, H, d), 160), randn((B, M, H, d), 161), randn((B, M, H, d), 162), randn((B, N, H, d), 163)
+    out, lse = bsa.cross_attn_fwd(g, q, k, v)
+    dq, dk, _ = bsa.cross_attn_bwd(g, q, k, v, out, lse, do)
+    want = oracle(q, k, v, torch.ones((B, M), dtype=torch.bool, device="cuda"), d ** -0.5, do)
+    for name, got in (("dq", dq), ("dk", dk)):
+        w = want[name][0]
+        rel = ((got.to(F64) - w).norm() / w.norm()).item()
+        assert rel <= math.sqrt(2 / 3) * R, (name, rel)
+
+
 def test_strided_and_shared_inputs():
     B, N, M, H, Hkv, d = 3, 150, 140, 4, 2, 64
     qkv = randn((B, N, 3, H, d), 90)
