@@ -87,6 +87,7 @@ bool aligned_as(const void* p, int type) {
 
 bool valid_cross(const bsa_cross_geom* g) {
   if (!g || g->B < 1 || g->H < 1 || g->Hkv < 1 || g->N < 1 || g->M < 1) return false;
+  if (g->M > (1 << 22)) return false;      // key tiles are a grid axis
   if (g->d != 64 && g->d != 128) return false;
   if (g->H % g->Hkv != 0 || g->H / g->Hkv > kCrossTile) return false;
   if ((long long)g->B * g->H > 65535) return false;

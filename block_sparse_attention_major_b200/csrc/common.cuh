@@ -115,8 +115,8 @@ __device__ __forceinline__ int tile_valid_count(const Geom& g, int tt, int ty, i
          min(kTileEdge, g.Ws - tx * kTileEdge);
 }
 
-// Does something once for each device (of the first 64; each time on others), such as setting a
-// kernel's attributes there: what it sets stays, and asking again costs a launch's host time.
+// Checks something once for each device (of the first 64; each time on others): what a device or a
+// kernel is does not change, and asking again costs a launch's host time.
 class OncePerDevice {
  public:
   template <typename F>

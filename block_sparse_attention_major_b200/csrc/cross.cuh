@@ -102,11 +102,11 @@ inline CrossWs cross_ws(const CrossGeom& g) {
 namespace cross {
 
 // Bounded wait for the phase of parity `parity`: each try suspends the thread for at most 200 ns, so
-// giving up takes between a tenth of a second and some two seconds. Gives up at once when another
+// giving up takes between a third of a second and seven seconds. Gives up at once when another
 // thread has set *abort; on time-out it sets *abort and the error bit. Kept short because it
 // stands at every hand-over of warps that run little else: with a clock in it, the code of the
 // waits alone displaced the others' from the instruction cache.
-constexpr int kWaitTries = 1 << 23;
+constexpr int kWaitTries = 1 << 25;
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1

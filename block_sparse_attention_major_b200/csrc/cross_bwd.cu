@@ -931,13 +931,9 @@ cudaError_t run_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtenso
                     const CUtensorMap& mdq, const BwdArgs& a, const __nv_bfloat16* out, const __nv_bfloat16* dout, const float* lse,
                     float2* stats, int* prefix, cudaStream_t s) {
   const CrossGeom& g = a.g;
-  static OncePerDevice once;
-  cudaError_t e = once([] {
-    const cudaError_t r =
-        cudaFuncSetAttribute(cross_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgQ<D>::kSmem);
-    if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(cross_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgK<D>::kSmem);
-  });
+  cudaError_t e = cudaFuncSetAttribute(cross_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgQ<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(cross_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgK<D>::kSmem);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)g.N * g.H, per = 4 * 256 / (D / 8);
   cross_stats_kernel<D><<<dim3((unsigned)((rows + per - 1) / per), g.B), 256, 0, s>>>(g, a.keys, out, dout, lse, stats, prefix);

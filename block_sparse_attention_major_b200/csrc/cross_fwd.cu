@@ -632,13 +632,14 @@ EncodeTiledFn encode_fn() {
 template <int D>
 cudaError_t run_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                     const FwdArgs& a, cudaStream_t s) {
+  // set anew for every call: a device reset forgets it
+  cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
   static OncePerDevice once;
-  cudaError_t e = once([] {
-    cudaError_t r = cudaFuncSetAttribute(cross_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
-    if (r != cudaSuccess) return r;
+  e = once([] {
     // A register split above what the launch provides would wait forever in setmaxnreg.
     cudaFuncAttributes fa;
-    r = cudaFuncGetAttributes(&fa, cross_fwd_kernel<D>);
+    const cudaError_t r = cudaFuncGetAttributes(&fa, cross_fwd_kernel<D>);
     if (r != cudaSuccess) return r;
     return fa.numRegs * kThreads < 128 * (2 * kRegsSoftmax + kRegsOut + kRegsControl) ? cudaErrorInvalidConfiguration
                                                                                     : cudaSuccess;

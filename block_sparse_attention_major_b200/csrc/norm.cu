@@ -570,14 +570,13 @@ int norm_blocks(const NormShape& n, long long rows, bool bwd) {
   return (int)(need < full ? need : full);
 }
 
-// `most`: the largest shared memory that a launch of this kernel takes (it needs leave above 48 KB,
-// static arrays included).
+// `most`: the largest shared memory that a launch of this kernel takes. Above 48 KB, static arrays
+// included, it needs leave, asked for at every launch (a device reset forgets it) and for the most,
+// so that launches of other sizes on other threads do not take it away.
 template <auto kKernel>
 cudaError_t start(const NormArgs& a, int blocks, int threads, size_t smem, size_t most, cudaStream_t s) {
-  if (most > 40 * 1024) {
-    static OncePerDevice once;
-    const cudaError_t e =
-        once([most] { return cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most); });
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
   }
   kKernel<<<blocks, threads, smem, s>>>(a);

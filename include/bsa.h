@@ -302,7 +302,7 @@ int bsa_layer_norm_bwd(const bsa_norm_shape* f, const void* x, const void* dy, c
  *   H, Hkv    query heads and key heads; Hkv divides H, query head h reads key head
  *             h / (H / Hkv); H / Hkv <= 128, B*H <= 65535
  *   d         head dimension, 64 or 128
- * with B*N*H < 2^31 and B*M*Hkv < 2^31. */
+ * with M <= 2^22, B*N*H < 2^31 and B*M*Hkv < 2^31. Outputs may not overlap inputs. */
 typedef struct bsa_cross_geom {
     int B;
     int H;

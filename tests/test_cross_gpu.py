@@ -368,3 +368,16 @@ def test_refusals():
         with pytest.raises(bsa.BsaError):
             bad()
     assert bsa.cross_workspace_bytes(bsa.CrossGeometry(1, 4, 3, 64, 1, 1)) == 0
+
+
+def test_offsets_past_32_bits():
+    # 2.3e9 elements of q and out: the last tokens are those of a call on them alone
+    import block_sparse_attention_major_b200 as bsa
+    N, H, d, M = 140000, 128, 128, 5
+    k, v = randn((1, M, 16, d), 170), randn((1, M, 16, d), 171)
+    q = torch.zeros((1, N, H, d), dtype=BF, device="cuda")
+    q[:, -300:] = randn((1, 300, H, d), 172)
+    out, lse = bsa.cross_attn_fwd(bsa.CrossGeometry(1, H, 16, d, N, M), q, k, v)
+    last, last_lse = bsa.cross_attn_fwd(bsa.CrossGeometry(1, H, 16, d, 300, M), q[:, -300:], k, v)
+    assert torch.equal(out[:, -300:], last) and torch.equal(lse[:, :, -300:], last_lse)
+    assert torch.equal(out[:, 7], out[:, N - 301])

@@ -264,3 +264,17 @@ def test_refusals():
         bsa.layer_norm_fwd(x, eps=-1.0)
     with pytest.raises(bsa.BsaError):
         bsa.layer_norm_fwd(torch.zeros((1, 16385), device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    import block_sparse_attention_major_b200 as bsa
+    rows, C = 1 << 20, 2100
+    x = torch.zeros((rows, C), dtype=BF, device="cuda")
+    x[-50:] = torch.randn((50, C), generator=torch.Generator().manual_seed(12)).to(BF).cuda()
+    y, mean, rstd = bsa.layer_norm_fwd(x)
+    want = bsa.layer_norm_fwd(x[-50:].clone())
+    for got, w in zip((y, mean, rstd), want):
+        assert torch.equal(got[-50:], w)
+    assert not y[:-50].any()
+    dx, _, _ = bsa.layer_norm_bwd(x, x, mean, rstd, dx=y)
+    assert torch.equal(dx[-50:], bsa.layer_norm_bwd(x[-50:].clone(), x[-50:].clone(), want[1], want[2])[0])

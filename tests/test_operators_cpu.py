@@ -31,7 +31,8 @@ def cross(lib, geom=(2, 4, 2, 64, 10, 12), st=None, q=P, k=P, v=P, kv_len=None, 
 @pytest.mark.parametrize("geom", [(0, 4, 2, 64, 10, 12), (2, 0, 2, 64, 10, 12), (2, 4, 0, 64, 10, 12), (2, 4, 3, 64, 10, 12),
                                   (2, 4, 2, 96, 10, 12), (2, 4, 2, 64, 0, 12), (2, 4, 2, 64, 10, 0), (2, 4, 2, 64, -1, 12),
                                   (1, 129, 1, 64, 10, 12), (65536, 1, 1, 64, 1, 1), (1, 32768, 32768, 64, 1 << 17, 12),
-                                  (1, 32768, 32768, 64, 10, 1 << 17), (1, 1, 1, 64, 10, 2147483647)], ids=str)
+                                  (1, 32768, 32768, 64, 10, 1 << 17), (1, 1, 1, 64, 10, 2147483647),
+                                  (1, 1, 1, 64, 10, (1 << 22) + 1)], ids=str)
 def test_cross_geometry_refused(lib, geom):
     import block_sparse_attention_major_b200 as bsa
     assert lib.bsa_cross_workspace_bytes(ctypes.byref(bsa.bsa_cross_geom(*geom))) == 0
