@@ -193,14 +193,14 @@ __device__ __forceinline__ void row_sum(float (&s)[S], int tpr, float* red) {
 }
 
 // Rows are taken in groups of U a lane group; all but one of a ring of groups are on their way to
-// shared memory while one is at work (E > 1). Four groups, fewer where T threads' pieces of them
-// are over 200 KB.
+// shared memory while one is at work (E > 1). Four groups, fewer where the pieces of an SM's
+// threads are over 200 KB.
 template <typename XT, int VPT, int U>
 constexpr int kFwdPieces = U* VPT* kPieces<XT>;
 template <typename XT, typename YT, int VPT, int U>
 constexpr int kBwdPieces = U* VPT*(kPieces<XT> + kPieces<YT>);
-constexpr int ring_depth(int pieces, int T) {
-  const int d = 204800 / (16 * pieces * T);
+constexpr int ring_depth(int pieces, int threads_sm) {
+  const int d = 204800 / (16 * pieces * threads_sm);
   return d < 1 ? 1 : d > 4 ? 4 : d;
 }
 
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
   __shared__ float red[2][U * 32];
   extern __shared__ uint4 ring[];         // [kDepth][piece][thread]
   constexpr bool kAhead = E > 1;
-  constexpr int P = kPieces<XT>, kDepth = ring_depth(kFwdPieces<XT, VPT, U>, T);
+  constexpr int P = kPieces<XT>, kDepth = ring_depth(kFwdPieces<XT, VPT, U>, T * kPerSm);
   const int tpr = a.tpr, t = threadIdx.x % tpr, sub = threadIdx.x / tpr, rpb = blockDim.x / tpr, C = a.C;
   const int plane = blockDim.x;
   const float inv_c = 1.0f / (float)C;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
   __shared__ float red[2][2 * U * 32];
   extern __shared__ uint4 ring[];         // [kDepth][piece][thread]
   constexpr bool kAhead = E > 1;
-  constexpr int PX = kPieces<XT>, PY = kPieces<YT>, kDepth = ring_depth(kBwdPieces<XT, YT, VPT, U>, T);
+  constexpr int PX = kPieces<XT>, PY = kPieces<YT>, kDepth = ring_depth(kBwdPieces<XT, YT, VPT, U>, T * kPerSm);
   const int tpr = a.tpr, t = threadIdx.x % tpr, sub = threadIdx.x / tpr, rpb = blockDim.x / tpr, C = a.C;
   const int plane = blockDim.x;
   const float inv_c = 1.0f / (float)C;
@@ -559,13 +559,13 @@ constexpr int kBwdU = E > 1 && VPT == 1 ? 2 : 1;
 // Blocks an SM that a kernel is built for: registers to hold everything (what does not fit goes
 // through L2, since the copies ahead leave L1 little: a backward pass with 216 bytes of it a
 // thread took twice as long).
-constexpr int per_sm(int vpt, int T, bool bwd) { return T > 256 ? 1 : vpt == 1 && !bwd ? 3 : 2; }
+constexpr int per_sm(int vpt, int T, bool bwd) { return T > 320 ? 1 : vpt == 1 && !bwd ? 3 : 2; }
 
 // Blocks of a launch: enough to fill the device, never more than there are rows for one each of a
 // block's lane groups.
 int norm_blocks(const NormShape& n, long long rows, bool bwd) {
   const long long step = n.threads / n.tpr, need = (rows + step - 1) / step;
-  const int T = n.threads > 256 ? n.threads : 256;
+  const int T = n.threads > 320 ? n.threads : n.threads > 256 ? 320 : 256;
   const long long full = (long long)kNormSms * (per_sm(n.vpt, T, bwd) * T / n.threads);
   return (int)(need < full ? need : full);
 }
@@ -587,14 +587,14 @@ cudaError_t start(const NormArgs& a, int blocks, int threads, size_t smem, size_
 template <typename XT, typename YT, int E, int VPT, int T>
 cudaError_t run_fwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
   constexpr int U = kFwdU<XT, E, VPT>, kPieces = kFwdPieces<XT, VPT, U>;
-  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T) * kPieces : 0;
+  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T * per_sm(VPT, T, false)) * kPieces : 0;
   return start<norm_fwd_kernel<XT, YT, E, VPT, U, T, per_sm(VPT, T, false)>>(a, blocks, n.threads, kThread * n.threads,
                                                                         kThread * T, s);
 }
 template <typename XT, typename YT, int E, int VPT, int T>
 cudaError_t run_bwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
   constexpr int U = kBwdU<E, VPT>, kPieces = kBwdPieces<XT, YT, VPT, U>;
-  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T) * kPieces : 0;
+  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T * per_sm(VPT, T, true)) * kPieces : 0;
   const size_t acc = n.tpr < n.threads && a.part ? 2 * sizeof(float) * a.C : 0;      // rows of at most 512
   return start<norm_bwd_kernel<XT, YT, E, VPT, U, T, per_sm(VPT, T, true)>>(
       a, blocks, n.threads, kThread * n.threads + acc, kThread * T + 2 * sizeof(float) * 512, s);
@@ -609,6 +609,7 @@ cudaError_t run_norm(const NormArgs& a, bool bwd, const NormShape& n, int blocks
   const bool wide = n.threads > 256;
   if (n.vpt == 1 && wide) return run_either<XT, YT, 1, 1, 640>(a, bwd, n, blocks, s);   // E = 1 only
   if (n.vpt == 1) return run_either<XT, YT, E, 1, 256>(a, bwd, n, blocks, s);
+  if (n.vpt == 2 && wide && n.threads <= 320) return run_either<XT, YT, E, 2, 320>(a, bwd, n, blocks, s);
   if (n.vpt == 2 && wide) return run_either<XT, YT, E, 2, 512>(a, bwd, n, blocks, s);
   if (n.vpt == 2) return run_either<XT, YT, E, 2, 256>(a, bwd, n, blocks, s);
   if (wide) return run_either<XT, YT, E, 4, 512>(a, bwd, n, blocks, s);
