@@ -559,14 +559,16 @@ constexpr int kBwdU = E > 1 && VPT == 1 ? 2 : 1;
 // Blocks an SM that a kernel is built for: registers to hold everything (what does not fit goes
 // through L2, since the copies ahead leave L1 little: a backward pass with 216 bytes of it a
 // thread took twice as long).
-constexpr int per_sm(int vpt, int T, bool bwd) { return T > 320 ? 1 : vpt == 1 && !bwd ? 3 : 2; }
+constexpr int per_sm(int vpt, int T, bool bwd, int E) {
+  return T > 320 ? 1 : vpt > 1 ? 2 : (bwd ? 2 : 3) + (E == 1 ? 1 : 0);
+}
 
 // Blocks of a launch: enough to fill the device, never more than there are rows for one each of a
 // block's lane groups.
-int norm_blocks(const NormShape& n, long long rows, bool bwd) {
+int norm_blocks(const NormShape& n, long long rows, bool bwd, int run) {
   const long long step = n.threads / n.tpr, need = (rows + step - 1) / step;
   const int T = n.threads > 320 ? n.threads : n.threads > 256 ? 320 : 256;
-  const long long full = (long long)kNormSms * (per_sm(n.vpt, T, bwd) * T / n.threads);
+  const long long full = (long long)kNormSms * (per_sm(n.vpt, T, bwd, run) * T / n.threads);
   return (int)(need < full ? need : full);
 }
 
@@ -587,16 +589,16 @@ cudaError_t start(const NormArgs& a, int blocks, int threads, size_t smem, size_
 template <typename XT, typename YT, int E, int VPT, int T>
 cudaError_t run_fwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
   constexpr int U = kFwdU<XT, E, VPT>, kPieces = kFwdPieces<XT, VPT, U>;
-  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T * per_sm(VPT, T, false)) * kPieces : 0;
-  return start<norm_fwd_kernel<XT, YT, E, VPT, U, T, per_sm(VPT, T, false)>>(a, blocks, n.threads, kThread * n.threads,
+  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T * per_sm(VPT, T, false, E)) * kPieces : 0;
+  return start<norm_fwd_kernel<XT, YT, E, VPT, U, T, per_sm(VPT, T, false, E)>>(a, blocks, n.threads, kThread * n.threads,
                                                                         kThread * T, s);
 }
 template <typename XT, typename YT, int E, int VPT, int T>
 cudaError_t run_bwd(const NormArgs& a, const NormShape& n, int blocks, cudaStream_t s) {
   constexpr int U = kBwdU<E, VPT>, kPieces = kBwdPieces<XT, YT, VPT, U>;
-  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T * per_sm(VPT, T, true)) * kPieces : 0;
+  constexpr size_t kThread = E > 1 ? 16 * ring_depth(kPieces, T * per_sm(VPT, T, true, E)) * kPieces : 0;
   const size_t acc = n.tpr < n.threads && a.part ? 2 * sizeof(float) * a.C : 0;      // rows of at most 512
-  return start<norm_bwd_kernel<XT, YT, E, VPT, U, T, per_sm(VPT, T, true)>>(
+  return start<norm_bwd_kernel<XT, YT, E, VPT, U, T, per_sm(VPT, T, true, E)>>(
       a, blocks, n.threads, kThread * n.threads + acc, kThread * T + 2 * sizeof(float) * 512, s);
 }
 
@@ -648,7 +650,7 @@ cudaError_t dispatch(const bsa_norm_shape& f, NormArgs& a, bool bwd, cudaStream_
   };
   const int run = allows(8) ? 8 : allows(2) ? 2 : 1;
   const NormShape n = norm_shape(f.C, bwd, !xb, run);
-  const int blocks = norm_blocks(n, f.rows, bwd);
+  const int blocks = norm_blocks(n, f.rows, bwd, run);
   a.tpr = n.tpr;
   a.slots = blocks + (a.w_items ? f.items : 1);
   if (blocks_out) *blocks_out = blocks;
@@ -663,7 +665,7 @@ cudaError_t dispatch(const bsa_norm_shape& f, NormArgs& a, bool bwd, cudaStream_
 size_t norm_workspace(const bsa_norm_shape& f) {
   int blocks = 0;                 // whatever the addresses allow
   for (const int run : {1, 2, 8}) {
-    const int n = norm_blocks(norm_shape(f.C, true, f.x_type == BSA_FP32, run), f.rows, true);
+    const int n = norm_blocks(norm_shape(f.C, true, f.x_type == BSA_FP32, run), f.rows, true, run);
     if (n > blocks) blocks = n;
   }
   return align256((size_t)(blocks + (f.w_per_item ? f.items : 1)) * f.C * 2 * sizeof(float));
