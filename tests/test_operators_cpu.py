@@ -139,22 +139,22 @@ def test_binding_passes_cross_attention_on(monkeypatch):
     import block_sparse_attention_major_b200 as bsa
     calls = []
     fake(monkeypatch, bsa, calls)
-    g = bsa.CrossGeometry(2, 4, 2, 64, 10, 12)
+    g = bsa.CrossGeometry(2, 4, 2, 64, 10, 11)
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
-    q, k, v, out, do = bf(2, 10, 4, 64), bf(2, 12, 2, 64), bf(2, 12, 2, 64), bf(2, 10, 4, 64), bf(2, 10, 4, 64)
+    q, k, v, out, do = bf(2, 10, 4, 64), bf(2, 11, 2, 64), bf(2, 11, 2, 64), bf(2, 10, 4, 64), bf(2, 10, 4, 64)
     lse, ws, n = torch.zeros(2, 4, 10), torch.zeros(4096, dtype=torch.uint8), torch.zeros(2, dtype=torch.int32)
-    m = torch.ones(2, 12, dtype=torch.bool)
+    m = torch.ones(2, 11, dtype=torch.bool)
     bsa.cross_attn_fwd(g, q, k, v, n, m, 0.5, out, lse, ws)
     name, a = calls[-1]
     assert name == "bsa_cross_attn_fwd" and a[1] is None
     assert a[2:] == (q.data_ptr(), k.data_ptr(), v.data_ptr(), n.data_ptr(), m.data_ptr(), 0.5, out.data_ptr(),
                      lse.data_ptr(), ws.data_ptr(), 4096, 0x5000)
-    dq, dk, dv = bf(2, 10, 4, 64), bf(2, 12, 2, 64), bf(2, 12, 2, 64)
-    kv = bf(2, 12, 2, 2, 64)
+    dq, dk, dv = bf(2, 10, 4, 64), bf(2, 11, 2, 64), bf(2, 11, 2, 64)
+    kv = bf(2, 11, 2, 2, 64)
     bsa.cross_attn_bwd(g, q, kv[:, :, 0], kv[:, :, 1], out, lse, do, None, None, None, dq, dk, dv, ws)
     name, a = calls[-1]
     st = a[1]._obj
-    assert list(st.q) == [2560, 256, 64] and list(st.k) == [3072, 256, 64] and list(st.v) == [3072, 256, 64]
+    assert list(st.q) == [2560, 256, 64] and list(st.k) == [2816, 256, 64] and list(st.v) == [2816, 256, 64]
     assert name == "bsa_cross_attn_bwd" and a[2:8] == (q.data_ptr(), kv.data_ptr(), kv.data_ptr() + 256, out.data_ptr(),
                                                       lse.data_ptr(), do.data_ptr())
     assert a[8:] == (None, None, 0.125, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), 4096, 0x5000)
