@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // may be the next unit's first). The warp runs whole; one lane issues.
       uint32_t nk = 0, nv = 0, np[2] = {0, 0}, nq[2] = {0, 0};
       auto wait = [&](uint32_t b, uint32_t ph) { return warp_wait(b, ph, abort, a.err); };
-      TileCursor cur, nxt;
+      TileCursor nxt;
       nxt.rows[0] = nxt.rows[1] = 0;
       nxt.open(a, blockIdx.x);
       auto scores = [&](int x) {
@@ -348,32 +348,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool ok = !nxt.valid || (scores(0) && (!nxt.has_b || scores(1)));
       while (ok && nxt.valid) {
-        cur = nxt;
-        nxt.next(a);
+        const bool first = nxt.kt == nxt.t0, last = nxt.kt == nxt.t1 - 1, has_b = nxt.has_b;
+        const uint32_t rows[2] = {nxt.rows[0], nxt.rows[1]};
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (x == 0 || cur.has_b) {
+          if (x == 0 || has_b) {
             const int s = (int)(nv % S);
             // the unit before must have been read out of O
-            if (cur.kt == cur.t0 && cur.rows[x] > 1 && !wait(bar.oempty(x), cur.rows[x] & 1)) { ok = false; break; }
+            if (first && rows[x] > 1 && !wait(bar.oempty(x), rows[x] & 1)) { ok = false; break; }
             if (x == 0 && !wait(bar.vfull(s), (nv / S) & 1)) { ok = false; break; }
             if (!wait(bar.pfull(x, 0), np[x] & 1)) { ok = false; break; }
             ptx::tc_fence_after();
             const uint32_t o_tmem = tmem + 256u + (uint32_t)(x * D), p_tmem = tmem + 128u * (uint32_t)x;
             const uint32_t v_smem = sbase + C::kV + s * C::kTile;
-            if (elect_one()) product_nn_half<D, 0>(o_tmem, p_tmem, 32, v_smem, cur.kt > cur.t0);
+            if (elect_one()) product_nn_half<D, 0>(o_tmem, p_tmem, 32, v_smem, !first);
             __syncwarp();
             if (!wait(bar.pfull(x, 1), np[x]++ & 1)) { ok = false; break; }
             ptx::tc_fence_after();
-            const bool release = x == 1 || !cur.has_b;
+            const bool release = x == 1 || !has_b;
             if (elect_one()) {
               product_nn_half<D, 1>(o_tmem, p_tmem, 32, v_smem, true);
-              if (cur.kt == cur.t1 - 1) ptx::mma_commit(bar.odone(x));
+              if (last) ptx::mma_commit(bar.odone(x));
               if (release) ptx::mma_commit(bar.vempty(s));
             }
             __syncwarp();
             nv += release;
           }
+          if (x == 0) nxt.next(a);            // behind a P V, which the pipe is still busy with
           if (nxt.valid && (x == 0 || nxt.has_b) && !scores(x)) { ok = false; break; }
         }
       }
