@@ -514,11 +514,14 @@ def cross_workspace_bytes(g: CrossGeometry) -> int:
 
 
 def alloc_cross_workspace(g: CrossGeometry, device=None) -> torch.Tensor:
-    """A zeroed device workspace of cross_attn_fwd and cross_attn_bwd (byte 0 = kernel error word)."""
+    """A device workspace of cross_attn_fwd and cross_attn_bwd, its header (byte 0 = kernel error word)
+    zeroed."""
     n = cross_workspace_bytes(g)
     if n == 0:
         raise ValueError("invalid geometry")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:256].zero_()
+    return ws
 
 
 def _need_strided(t: torch.Tensor, shape, name: str) -> None:
