@@ -66,8 +66,8 @@ __device__ __forceinline__ bool all_set(uint4 w) { return (w.x & w.y & w.z & w.w
 // -------------------------------------------------------------------- workspace layout
 // [0, 256)  error word; then, 256-aligned: plan int2 [B], packed key bits u32 [B, 4 nkt], prefix of
 // the items' key tiles int [B + 1], row statistics float2 [B, H, N] (backward), and one region
-// that the forward pass uses for the partial results of split keys, the backward pass for the
-// partial dk, dv of its blocks.
+// that the forward pass uses for the partial results of split keys, the backward pass for those of
+// dq and then for the partial dk, dv of its blocks.
 struct CrossWs {
   size_t plan, bits, prefix, stats, part, total;
 };
@@ -76,12 +76,15 @@ struct CrossWs {
 // takes a launch and some 3 us, so short walks stay whole (one query and 12 heads over 512 keys:
 // 11.0 us, in 4 parts 6.3 + 3.0 us and the launch), and a part has at least two tiles (1024 keys:
 // 11.1 us in parts of 4 tiles, 7.1 us in parts of 1, the join 2.9 and 4.1 us).
-inline int cross_splits(const CrossGeom& g) {
-  const long long units = (long long)g.B * g.Hkv * ceil_div(g.nqt, 2);
+inline int cross_parts(const CrossGeom& g, int row_units) {
+  const long long units = (long long)g.B * g.Hkv * row_units;
   if (units * 2 > kCrossSms || g.nkt < 8) return 1;
   const long long s = kCrossSms / units, most = g.nkt / 2;
   return (int)(s < most ? s : most);
 }
+
+inline int cross_splits(const CrossGeom& g) { return cross_parts(g, ceil_div(g.nqt, 2)); }   // forward
+inline int cross_dq_splits(const CrossGeom& g) { return cross_parts(g, g.nqt); }
 
 inline CrossWs cross_ws(const CrossGeom& g) {
   CrossWs w;
@@ -93,7 +96,10 @@ inline CrossWs cross_ws(const CrossGeom& g) {
   w.part = off;
   const int s = cross_splits(g);
   const size_t fwd = s > 1 ? (size_t)s * g.B * g.N * g.H * (g.d + 1) * sizeof(float) : 0;
-  const size_t bwd = (size_t)kCrossSms * 2 * 2 * kCrossTile * g.d * sizeof(float);
+  const int sq = cross_dq_splits(g);
+  const size_t dq = sq > 1 ? (size_t)sq * g.B * g.N * g.H * g.d * sizeof(float) : 0;
+  const size_t dkv = (size_t)kCrossSms * 2 * 2 * kCrossTile * g.d * sizeof(float);
+  const size_t bwd = dq > dkv ? dq : dkv;             // dq is joined before dk, dv begin
   w.total = align256(off + (fwd > bwd ? fwd : bwd));
   return w;
 }

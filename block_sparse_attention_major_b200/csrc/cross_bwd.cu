@@ -42,10 +42,12 @@ struct BwdArgs {
   const int* prefix;                // key tiles of the items before b; null: every item has nkt
   int kb_mul, vb_mul, qb_mul;
   __nv_bfloat16 *dk, *dv;
-  float* part;                      // cut units: [CTA][first / last][dk, dv][128][D]
+  float* part;                      // cut units: [CTA][first / last][dk, dv][128][D]; before that, with split
+                                    // keys, dq unscaled: [splits, B, N, H, D]
+  int splits;                       // parts of the keys of a dq unit
   uint32_t* err;
   float scale, scale_log2;
-  FastDiv by_nqt;
+  FastDiv by_nqt, by_splits;
 };
 
 __device__ __forceinline__ int key_tiles(const BwdArgs& a, int b) {
@@ -83,7 +85,9 @@ struct CfgQ {
   static_assert(kSmem <= 232448, "shared memory");
 };
 
-template <int D>
+// kSplit: the keys of a unit in parts (few query rows); kept out of the other form, which it slowed
+// by 5 %.
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -123,12 +127,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;                 // S buffers at 0 and 128, T at 256, dq at 384
 
   auto wait = [&](uint32_t b, uint32_t ph) { return wait_phase(b, ph, abort, a.err); };
-  // unit -> (query tile, key head, item); query tiles fastest, so that neighbours share keys
-  auto decode = [&](int u, int& qt, int& hkv, int& b) {
-    const int bh = (int)a.by_nqt.q((uint32_t)u);
-    qt = u - bh * g.nqt;
+  // unit -> (query tile, part of the keys, key head, item); query tiles fastest, so that neighbours
+  // share keys
+  auto decode = [&](int u, int& qt, int& hkv, int& b, int& part) {
+    const int rest = (int)a.by_nqt.q((uint32_t)u);
+    qt = u - rest * g.nqt;
+    const int bh = kSplit ? (int)a.by_splits.q((uint32_t)rest) : rest;
+    part = kSplit ? rest - bh * a.splits : 0;
     b = (int)g.by_hkv.q((uint32_t)bh);
     hkv = bh - b * g.Hkv;
+  };
+  // key tiles of a part: [t0, t1)
+  auto tiles_of = [&](int nt, int part, int& t0, int& t1) {
+    t0 = 0;
+    t1 = nt;
+    if (kSplit) {
+      t0 = (int)((long long)nt * part / a.splits);
+      t1 = (int)((long long)nt * (part + 1) / a.splits);
+    }
   };
 
   if (warp == 8) {
@@ -138,19 +154,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const uint32_t bytes = (uint32_t)(g.G * g.tpt * D * 2);
       for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        int qt, hkv, b;
-        decode(u, qt, hkv, b);
-        const int nt = key_tiles(a, b);
+        int qt, hkv, b, part, t0, t1;
+        decode(u, qt, hkv, b, part);
+        tiles_of(key_tiles(a, b), part, t0, t1);
         if (u + (int)gridDim.x < units) {           // the next unit's rows come from HBM meanwhile
-          int qf, hf, bf;
-          decode(u + (int)gridDim.x, qf, hf, bf);
+          int qf, hf, bf, pf;
+          decode(u + (int)gridDim.x, qf, hf, bf, pf);
 #pragma unroll
           for (int cb = 0; cb < D / 64; ++cb) {
             tma_prefetch_4d(&tmQ, cb * 64, hf * g.G, qf * g.tpt, bf * a.qb_mul);
             tma_prefetch_4d(&tmDo, cb * 64, hf * g.G, qf * g.tpt, bf);
           }
         }
-        if (nt == 0) continue;
+        if (t0 == t1) continue;
         if (nq > 0 && !wait(qempty, (nq - 1) & 1)) break;
         ptx::mbar_arrive_expect_tx(qfull, bytes);
 #pragma unroll
@@ -166,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int cb = 0; cb < D / 64; ++cb)
           tma_load_4d(sbase + C::kDo + cb * 16384, &tmDo, dofull, cb * 64, hkv * g.G, qt * g.tpt, b);
         ++nq;
-        for (int i = 0; i < nt; ++i) {
+        for (int i = t0; i < t1; ++i) {
           const int s = (int)(nv % VS);
           if (!wait(vempty(s), ((nv / VS) & 1) ^ 1)) { ok = false; break; }
           ptx::mbar_arrive_expect_tx(vfull(s), C::kTile);
@@ -194,10 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < KS; ++s) land[s] = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      int qt, hkv, b;
-      decode(u, qt, hkv, b);
-      const int len = item_keys(a.keys, b, g.M).x, nt = (len + kCrossTile - 1) / kCrossTile;
-      for (int i = 0; i < nt; ++i) {
+      int qt, hkv, b, part, t0, t1;
+      decode(u, qt, hkv, b, part);
+      const int len = item_keys(a.keys, b, g.M).x;
+      tiles_of((len + kCrossTile - 1) / kCrossTile, part, t0, t1);
+      for (int i = t0; i < t1; ++i) {
         const int s = (int)(nk % KS);
         if (!warp_wait(kempty(s), ((nk / KS) & 1) ^ 1, abort, a.err)) { ok = false; break; }
         const uint4 w = tile_bits(a.keys, b, i, g.nkt, len);
@@ -263,9 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      int qt, hkv, b;
-      decode(u, qt, hkv, b);
-      const int nt = key_tiles(a, b);
+      int qt, hkv, b, part, t0, t1;
+      decode(u, qt, hkv, b, part);
+      tiles_of(key_tiles(a, b), part, t0, t1);
+      const int nt = t1 - t0;
       if (nt == 0) continue;
       if (!all_wait(qfull, nq & 1) || !scores(nt == 1)) break;
       if (!all_wait(dofull, nq & 1) || !tee(nt == 1)) break;
@@ -308,6 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       in = bar_all(1, 256, in);
       if (!in) return false;
       ptx::tc_fence_after();
+      int qt = 0, hkv = 0, b = 0, part = 0;
+      if (kSplit || threadIdx.x == 0) decode(from, qt, hkv, b, part);
+      const long long at = kSplit ? stats_at(a, b, hkv, qt, row) : 0;          // (b, head, token)
       const uint32_t o_tmem = tmem + 384u + (uint32_t)(half * (D / 2)) + lane_base;
 #pragma unroll 1
       for (int ch = 0; ch < D / 64; ++ch) {
@@ -319,16 +340,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
+        if (kSplit) {
+          // [part][B, H, N][D]: the join turns them into rows of tokens
+          if (at >= 0) {
+            uint4* dst = reinterpret_cast<uint4*>(a.part + (((long long)part * g.B * g.H * g.N + at) * D +
+                                                            half * (D / 2) + 32 * ch));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+          continue;
+        }
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           pk[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * a.scale, __uint_as_float(o[2 * k + 1]) * a.scale);
         put_row32(smem + C::kOut, row, half * (D / 64) + ch, pk);
       }
+      if (kSplit) return true;
       fence_proxy_async();
       bar_sync(1, 256);
       if (threadIdx.x == 0) {
-        int qt, hkv, b;
-        decode(from, qt, hkv, b);
 #pragma unroll
         for (int cb = 0; cb < D / 64; ++cb)
           tma_store_4d(&tmDq, sbase + C::kOut + cb * 16384, cb * 64, hkv * g.G, qt * g.tpt, b);
@@ -337,11 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      int qt, hkv, b;
-      decode(u, qt, hkv, b);
+      int qt, hkv, b, part, t0, t1;
+      decode(u, qt, hkv, b, part);
       const int2 ik = item_keys(a.keys, b, g.M);
       const int nt = (ik.x + kCrossTile - 1) / kCrossTile;
-      if (nt == 0) {
+      tiles_of(nt, part, t0, t1);
+      if (t0 == t1) {
         if (held >= 0 && !finish(held, true)) break;
         held = -1;
         if (!finish(u, false)) break;
@@ -350,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 st = row_stats(a, b, hkv, qt, row);
       const uint64_t cc = f2(c, c), mm = f2(-st.x, -st.x);
       uint64_t dd = f2(-st.y, -st.y);
-      for (int i = 0; i < nt; ++i, ++n) {
+      for (int i = t0; i < t1; ++i, ++n) {
         const uint4 w4 = tile_bits(a.keys, b, i, g.nkt, ik.x);
         const bool full = all_set(w4);
         const uint32_t w[2] = {half ? w4.z : w4.x, half ? w4.w : w4.y};
@@ -864,6 +895,27 @@ __global__ void __launch_bounds__(16 * D / 4) cross_dkv_join_kernel(BwdArgs a, i
   *reinterpret_cast<uint2*>(a.dk + at) = make_uint2(pack_bf16x2(sk.x, sk.y), pack_bf16x2(sk.z, sk.w));
 }
 
+// dq from the parts of split keys, added in their order: four neighbouring elements a thread.
+template <int D>
+__global__ void __launch_bounds__(256) cross_dq_join_kernel(CrossGeom g, int splits, float scale,
+                                                            const float* __restrict__ part,
+                                                            __nv_bfloat16* __restrict__ dq) {
+  const long long rows = (long long)g.B * g.N * g.H;
+  const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / (D / 4);
+  const int c4 = threadIdx.x % (D / 4);
+  if (at >= rows) return;
+  const int head = (int)(at % g.H);
+  const long long bn = at / g.H, b = bn / g.N, tok = bn % g.N;
+  const float4* p = reinterpret_cast<const float4*>(part) + ((b * g.H + head) * g.N + tok) * (D / 4) + c4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < splits; ++i) {
+    const float4 v = p[(long long)i * rows * (D / 4)];
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  *reinterpret_cast<uint2*>(dq + at * D + 4 * c4) =
+      make_uint2(pack_bf16x2(s.x * scale, s.y * scale), pack_bf16x2(s.z * scale, s.w * scale));
+}
+
 // Row statistics: (lse / log 2, sum over the row of do out), one row of D elements by D/8 lanes,
 // four rows a thread so that enough loads are in flight. A row without a key gets lse = +inf,
 // which makes its probabilities zero. Grid: rows of an item, item. One block also writes the
@@ -929,9 +981,10 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(CrossGeom g, KeySet ke
 template <int D>
 cudaError_t run_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk, const CUtensorMap& mv,
                     const CUtensorMap& mdq, const BwdArgs& a, const __nv_bfloat16* out, const __nv_bfloat16* dout, const float* lse,
-                    float2* stats, int* prefix, cudaStream_t s) {
+                    float2* stats, int* prefix, __nv_bfloat16* dq, cudaStream_t s) {
   const CrossGeom& g = a.g;
-  cudaError_t e = cudaFuncSetAttribute(cross_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgQ<D>::kSmem);
+  const auto dq_kernel = a.splits > 1 ? cross_dq_kernel<D, true> : cross_dq_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgQ<D>::kSmem);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(cross_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgK<D>::kSmem);
   if (e != cudaSuccess) return e;
@@ -940,12 +993,18 @@ cudaError_t run_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtenso
   count_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int units = g.B * g.Hkv * g.nqt;
-  cross_dq_kernel<D><<<units < kCrossSms ? units : kCrossSms, kThreads, CfgQ<D>::kSmem, s>>>(mq, mdo, mk, mv, mdq, a,
-                                                                                               units);
+  const int units = g.B * g.Hkv * a.splits * g.nqt;
+  dq_kernel<<<units < kCrossSms ? units : kCrossSms, kThreads, CfgQ<D>::kSmem, s>>>(mq, mdo, mk, mv, mdq, a, units);
   count_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (a.splits > 1) {
+    const long long quads = (long long)g.B * g.N * g.H * (D / 4);
+    cross_dq_join_kernel<D><<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(g, a.splits, a.scale, a.part, dq);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   const long long steps = (long long)g.B * g.Hkv * g.nkt * g.nqt;
   const int grid = (int)(steps < kCrossSms ? steps : kCrossSms);
   cross_dkv_kernel<D><<<grid, kThreads, CfgK<D>::kSmem, s>>>(mq, mdo, mk, mv, a);
@@ -986,6 +1045,8 @@ cudaError_t launch_cross_bwd(const CrossCall& c, const void* out, const float* l
   a.err = reinterpret_cast<uint32_t*>(c.ws);
   a.scale = c.scale;
   a.by_nqt = FastDiv((uint32_t)g.nqt);
+  a.splits = cross_dq_splits(g);
+  a.by_splits = FastDiv((uint32_t)a.splits);
   a.scale_log2 = c.scale * 1.4426950408889634f;
   const CrossStride dense = {(long long)g.N * g.H * g.d, (long long)g.H * g.d, g.d};
   CUtensorMap mq, mdo, mk, mv, mdq;
@@ -997,8 +1058,9 @@ cudaError_t launch_cross_bwd(const CrossCall& c, const void* out, const float* l
     return cudaErrorInvalidValue;
   const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(out);
   const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(dout);
-  return g.d == 128 ? run_bwd<128>(mq, mdo, mk, mv, mdq, a, o, d, lse, stats, prefix, s)
-                    : run_bwd<64>(mq, mdo, mk, mv, mdq, a, o, d, lse, stats, prefix, s);
+  __nv_bfloat16* q = static_cast<__nv_bfloat16*>(dq);
+  return g.d == 128 ? run_bwd<128>(mq, mdo, mk, mv, mdq, a, o, d, lse, stats, prefix, q, s)
+                    : run_bwd<64>(mq, mdo, mk, mv, mdq, a, o, d, lse, stats, prefix, q, s);
 }
 
 }  // namespace bsa
