@@ -608,14 +608,18 @@ cudaError_t run_either(const NormArgs& a, bool bwd, const NormShape& n, int bloc
 }
 template <typename XT, typename YT, int E>
 cudaError_t run_norm(const NormArgs& a, bool bwd, const NormShape& n, int blocks, cudaStream_t s) {
-  const bool wide = n.threads > 256;
-  if (n.vpt == 1 && wide) return run_either<XT, YT, 1, 1, 640>(a, bwd, n, blocks, s);   // E = 1 only
+  // what norm_shape gives for these rows, and nothing else
+  if constexpr (E == 1) {
+    if (n.vpt == 1 && n.threads > 256) return run_either<XT, YT, E, 1, 640>(a, bwd, n, blocks, s);
+  } else {
+    if (n.vpt == 2 && n.threads <= 256) return run_either<XT, YT, E, 2, 256>(a, bwd, n, blocks, s);
+    if (n.vpt == 2 && n.threads <= 320) return run_either<XT, YT, E, 2, 320>(a, bwd, n, blocks, s);
+    if constexpr (E >= 4 && sizeof(XT) == 2)        // forward only: the backward pass has 4 slots past 256 threads
+      if (n.vpt == 4 && n.threads <= 256) return run_fwd<XT, YT, E, 4, 256>(a, n, blocks, s);
+  }
   if (n.vpt == 1) return run_either<XT, YT, E, 1, 256>(a, bwd, n, blocks, s);
-  if (n.vpt == 2 && wide && n.threads <= 320) return run_either<XT, YT, E, 2, 320>(a, bwd, n, blocks, s);
-  if (n.vpt == 2 && wide) return run_either<XT, YT, E, 2, 512>(a, bwd, n, blocks, s);
-  if (n.vpt == 2) return run_either<XT, YT, E, 2, 256>(a, bwd, n, blocks, s);
-  if (wide) return run_either<XT, YT, E, 4, 512>(a, bwd, n, blocks, s);
-  return run_fwd<XT, YT, E, 4, 256>(a, n, blocks, s);       // the backward pass has 4 slots only past 256 threads
+  if (n.vpt == 2) return run_either<XT, YT, E, 2, 512>(a, bwd, n, blocks, s);
+  return run_either<XT, YT, E, 4, 512>(a, bwd, n, blocks, s);
 }
 
 NormArgs norm_args(const bsa_norm_shape& f) {
