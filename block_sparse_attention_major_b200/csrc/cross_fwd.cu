@@ -360,10 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 2; ++x) {
           if (x == 0 || has_b) {
             const int s = (int)(nv % S);
-            // the unit before must have been read out of O
-            if (first && rows[x] > 1 && !wait(bar.oempty(x), rows[x] & 1)) { ok = false; break; }
             if (x == 0 && !wait(bar.vfull(s), (nv / S) & 1)) { ok = false; break; }
             if (!wait(bar.pfull(x, 0), np[x] & 1)) { ok = false; break; }
+            // The unit before must have been read out of O. Behind the probabilities, not ahead of
+            // them: this warp passes over units without keys, whose phases of oempty it does not see,
+            // and the probabilities say that the softmax has seen all but the last (a wait that is
+            // two phases behind looks complete).
+            if (first && rows[x] > 1 && !wait(bar.oempty(x), rows[x] & 1)) { ok = false; break; }
             ptx::tc_fence_after();
             const uint32_t o_tmem = tmem + 256u + (uint32_t)(x * D), p_tmem = tmem + 128u * (uint32_t)x;
             const uint32_t v_smem = sbase + C::kV + s * C::kTile;

@@ -381,3 +381,24 @@ def test_offsets_past_32_bits():
     last, last_lse = bsa.cross_attn_fwd(bsa.CrossGeometry(1, H, 16, d, 300, M), q[:, -300:], k, v)
     assert torch.equal(out[:, -300:], last) and torch.equal(lse[:, :, -300:], last_lse)
     assert torch.equal(out[:, 7], out[:, N - 301])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_items_without_keys_between_many_units(d):
+    # one key tile, five items of which two are empty, several units of each a block: every item's
+    # rows are those of a call on it alone, and the same again
+    import block_sparse_attention_major_b200 as bsa
+    B, N, M, H = 5, 9000, 100, 12
+    q, k, v = randn((B, N, H, d), 180), randn((B, M, H, d), 181), randn((B, M, H, d), 182)
+    lens = [M, 0, M, 0, 77]
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    g, one = bsa.CrossGeometry(B, H, H, d, N, M), bsa.CrossGeometry(1, H, H, d, N, M)
+    ws = bsa.alloc_cross_workspace(g)
+    want = [bsa.cross_attn_fwd(one, q[b:b + 1], k[b:b + 1], v[b:b + 1], n[b:b + 1]) for b in range(B)]
+    for _ in range(4):
+        out, lse = bsa.cross_attn_fwd(g, q, k, v, n, ws=ws)
+        torch.cuda.synchronize()
+        assert bsa.read_error(ws) == 0
+        for b in range(B):
+            assert torch.equal(out[b:b + 1], want[b][0]) and torch.equal(lse[b:b + 1], want[b][1])
+            assert lens[b] or not out[b].any()
