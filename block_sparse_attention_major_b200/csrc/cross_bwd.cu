@@ -324,6 +324,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0, nd = 0;
     bool ok = true;
     int held = -1;                                  // the unit whose gradient is still in the accumulator
+    // A warp whose wait ran out says so at the next barrier of the eight warps before it leaves: others
+    // may have seen the same phase complete, and they would wait there for good. There always is
+    // one (a unit whose tiles are worked on is finished later), and no wait stands between the two
+    // barriers of finish().
+    auto give_up = [&] {
+      bar_all(1, 256, false);
+      return false;
+    };
     // Waits for the last product of unit `from` (none if it has no key) and stores its block.
     auto finish = [&](int from, bool any) {
       bool in = !any || warp_wait(done, nd & 1, abort, a.err);
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t w[2] = {half ? w4.z : w4.x, half ? w4.w : w4.y};
         const uint32_t s_tmem = tmem + 128u * (n & 1) + 64u * (uint32_t)half + lane_base;
         const uint32_t t_tmem = tmem + 256u + 64u * (uint32_t)half + lane_base;
-        if (!warp_wait(sfull((int)(n & 1)), (n >> 1) & 1, abort, a.err)) { ok = false; break; }
+        if (!warp_wait(sfull((int)(n & 1)), (n >> 1) & 1, abort, a.err)) { ok = give_up(); break; }
         ptx::tc_fence_after();
         uint32_t p[64];
         tmem_ld_x32(s_tmem, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
@@ -438,6 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long at = stats_at(a, b, hkv, qt, row);
             if (half == 0 && at >= 0) a.stats[at].y = sum;
           }
+        } else if (!ok) {
+          give_up();
         }
         if (!ok) break;
         ptx::tc_fence_after();

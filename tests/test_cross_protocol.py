@@ -14,6 +14,10 @@ An mbarrier's test for parity P succeeds when the phase in progress has the othe
 thread that has not seen the phase before the awaited one may pass two phases early. The issuer
 that waited for the block before O to be read out ahead of the new unit's probabilities did so
 behind units without keys; the model shows it.
+
+The second model is of the elementwise warps of the dq kernel when a bounded wait runs out: the
+eight warps meet at barriers that wait without a limit, so whoever gives up has to leave together
+with the others.
 """
 import random
 
@@ -206,3 +210,98 @@ def test_waiting_for_o_ahead_of_the_probabilities_is_caught():
         except Stale:
             caught += 1
     assert caught
+
+
+DQ_WARPS = 8
+
+
+def run_dq_give_up(units, seed, leave_alone=False):
+    """units: key tiles. The products stop at a random point, and some time later a wait elsewhere
+    runs out; each warp sees that at its own time. True if all warps leave. leave_alone: a warp
+    whose wait ran out goes without a word."""
+    rng = random.Random(seed)
+    phases = [("s", "t")] * sum(units)
+    last = rng.randint(0, 2 * len(phases))                  # products that are still done
+    done = {"s": 0, "t": 0, "out": 0}
+    abort = [False]
+    met, votes = [0], {}
+
+    def barrier(mine, vote):                                # of all warps; whether all said yes
+        votes[mine] = votes.get(mine, True) and vote
+        met[0] += 1
+        return lambda: met[0] >= DQ_WARPS * (mine + 1)
+
+    def warp():
+        n = {"s": 0, "t": 0, "out": 0}
+        gen, held = 0, False
+
+        def reached(kind):
+            # as wait_phase: the phase first, then the flag
+            return lambda: done[kind] > n[kind] or abort[0]
+
+        def taken(kind):
+            ok = done[kind] > n[kind]
+            n[kind] += 1
+            return ok
+
+        for tiles in units + [None]:
+            if not tiles:                                   # no keys, or the end
+                steps = (["out"] if held else []) + (["empty"] if tiles == 0 else [])
+                held = False
+            else:
+                steps = []
+                for i in range(tiles):
+                    steps += ["s"] + (["out"] if held else []) + ["t"]
+                    held = False
+                held = True
+            for step in steps:
+                ok = True
+                if step != "empty":
+                    yield reached(step)
+                    ok = taken(step)
+                if step in ("out", "empty") or (step == "t" and tiles == 1):
+                    yield barrier(gen, ok)
+                    ok, gen = votes[gen], gen + 1
+                    if not ok:
+                        return
+                    if step != "t":
+                        yield barrier(gen, True)
+                        gen += 1
+                elif not ok:
+                    if not leave_alone:
+                        yield barrier(gen, False)
+                    return
+
+    def products():
+        for i in range(last):
+            done["s" if i % 2 == 0 else "t"] += 1
+            done["out"] = sum(done["t"] >= sum(units[:u + 1]) for u in range(len(units)) if units[u])
+            yield lambda: True
+
+    def clock():
+        for _ in range(rng.randint(0, 60)):
+            yield lambda: True
+        abort[0] = True
+
+    agents = [warp() for _ in range(DQ_WARPS)] + [products(), clock()]
+    conds = [next(a, None) for a in agents]
+    while any(conds[:DQ_WARPS]):
+        ready = [i for i, c in enumerate(conds) if c and c()]
+        if not ready:
+            return False
+        i = rng.choice(ready)
+        conds[i] = next(agents[i], None)
+    return True
+
+
+DQ_UNITS = [[1], [2], [3, 1, 0, 2], [1, 1, 1], [0, 2, 2], [4, 4], [0, 0]]
+
+
+@pytest.mark.parametrize("units", DQ_UNITS, ids=str)
+def test_dq_warps_leave_together(units):
+    assert all(run_dq_give_up(units, seed) for seed in range(500))
+
+
+def test_a_dq_warp_that_leaves_alone_is_caught():
+    for units in ([3, 1, 0, 2], [4, 4], [2]):
+        assert not all(run_dq_give_up(units, seed, leave_alone=True) for seed in range(2000))
