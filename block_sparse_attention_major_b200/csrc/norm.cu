@@ -119,6 +119,9 @@ __device__ __forceinline__ void copy_slot(uint4* dst, int plane, const T* row, i
   }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Copies of one thread land in any order: a place must not be the target of a second one before
+// the first has been waited for. Zero fills past an item's rows are still under way when its last
+// row is done.
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -326,6 +329,7 @@ __global__ void __launch_bounds__(T, kPerSm) norm_fwd_kernel(NormArgs a) {
         }
       }
     }
+    if (kAhead) copies_wait<0>();         // see copies_wait: the next item starts at the first stage again
     r0 = end;
   }
 }
@@ -453,6 +457,7 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
         }
       }
     }
+    if (kAhead) copies_wait<0>();
     if (a.part) {
       // this block's partial row of the item: block + item counts up along the blocks' ranges,
       // so no two (block, item) pairs share it

@@ -278,3 +278,22 @@ def test_offsets_past_32_bits():
     assert not y[:-50].any()
     dx, _, _ = bsa.layer_norm_bwd(x, x, mean, rstd, dx=y)
     assert torch.equal(dx[-50:], bsa.layer_norm_bwd(x[-50:].clone(), x[-50:].clone(), want[1], want[2])[0])
+
+
+@pytest.mark.parametrize("C", [40, 128, 258, 1536, 5120])
+def test_many_items_a_block(C):
+    # a block's range meets several items: each item's rows are those of a call on it alone
+    import block_sparse_attention_major_b200 as bsa
+    B, N = 3000, 3
+    for xt in (BF, F32):
+        x, dy, w, b = (t.cuda() for t in make((B, N, C), xt, BF, "item", 60 + C))
+        for _ in range(3):
+            y, mean, rstd = bsa.layer_norm_fwd(x, w, b, out_dtype=BF)
+            dx, dw, db = bsa.layer_norm_bwd(x, dy, mean, rstd, w)
+            for i in (0, 1, 7, 501, 1500, 1501, 2222, B - 1):
+                y1, m1, r1 = bsa.layer_norm_fwd(x[i], w[i], b[i], out_dtype=BF)
+                dx1, _, _ = bsa.layer_norm_bwd(x[i], dy[i], m1, r1, w[i])
+                assert torch.equal(y[i], y1) and torch.equal(mean[i], m1) and torch.equal(dx[i], dx1)
+            h = (x.double() - mean.double()[..., None]) * rstd.double()[..., None]
+            near(dw, (dy.double() * h).sum(1).cpu(), (dy.double() * h).abs().sum(1).cpu(), "dweight")
+            near(db, dy.double().sum(1).cpu(), dy.double().abs().sum(1).cpu(), "dbias")
