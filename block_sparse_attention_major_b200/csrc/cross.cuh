@@ -174,6 +174,8 @@ __device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// Whole warps only, and converged ones (as with the tcgen05 reads and writes of TMEM): a __syncwarp
+// stands between them and a branch that only some lanes take.
 // A barrier of `threads` threads that also tells all of them whether all said yes: after a bounded
 // wait, so that threads whose wait ran out and threads whose did not leave together.
 __device__ __forceinline__ bool bar_all(int id, int threads, bool yes) {

@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool in = !any || warp_wait(done, nd & 1, abort, a.err);
       nd += any;
       if (threadIdx.x == 0) store_read();           // the staging is free again
+      __syncwarp();
       in = bar_all(1, 256, in);
       if (!in) return false;
       ptx::tc_fence_after();
@@ -346,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t o_tmem = tmem + 384u + (uint32_t)(half * (D / 2)) + lane_base;
 #pragma unroll 1
       for (int ch = 0; ch < D / 64; ++ch) {
+        __syncwarp();                               // lanes without a row of their own stored nothing
         uint32_t o[32], pk[16];
         if (any) {
           tmem_ld_x32(o_tmem + 32 * ch, o);
@@ -445,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dd = f2(-sum, -sum);
             const long long at = stats_at(a, b, hkv, qt, row);
             if (half == 0 && at >= 0) a.stats[at].y = sum;
+            __syncwarp();
           }
         } else if (!ok) {
           give_up();
@@ -830,22 +833,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t o_tmem = tmem + 256u + (uint32_t)(half * D) + lane_base;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
+        __syncwarp();                               // keys past M were not stored
         uint32_t o[32];
         tmem_ld_x32(o_tmem + 32 * ch, o);
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = valid ? __float_as_uint(__uint_as_float(o[k]) * sc) : 0u;
         if (whole) {
-          if (key >= g.M) continue;
-          uint4* dst = reinterpret_cast<uint4*>((half ? a.dk : a.dv) + (((long long)b * g.M + key) * g.Hkv + hkv) * D + 32 * ch);
+          if (key < g.M) {
+            uint4* dst = reinterpret_cast<uint4*>((half ? a.dk : a.dv) + (((long long)b * g.M + key) * g.Hkv + hkv) * D + 32 * ch);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 v;
-            v.x = pack_bf16x2(__uint_as_float(o[8 * k + 0]), __uint_as_float(o[8 * k + 1]));
-            v.y = pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3]));
-            v.z = pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5]));
-            v.w = pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]));
-            dst[k] = v;
+            for (int k = 0; k < 4; ++k) {
+              uint4 v;
+              v.x = pack_bf16x2(__uint_as_float(o[8 * k + 0]), __uint_as_float(o[8 * k + 1]));
+              v.y = pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3]));
+              v.z = pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5]));
+              v.w = pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]));
+              dst[k] = v;
+            }
           }
         } else {
           // a cut unit is the first or the last of this CTA's range

@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(bar.lfull(x), nl[x]++ & 1, abort, a.err) &&
              (!any || warp_wait(bar.odone(x), no[x]++ & 1, abort, a.err));
         if (threadIdx.x == 256) store_read();                 // the staging is free again
+        __syncwarp();
         ok = bar_all(1, 128, ok);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -421,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = row < g.G * g.tpt && tok < g.N;
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
+          __syncwarp();                           // lanes without a row of their own stored nothing
           uint32_t o[32];
           if (any) {
             tmem_ld_x32(o_tmem + 32 * ch, o);
@@ -447,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar.oempty(x));
+        __syncwarp();
         if (a.splits == 1) {
           fence_proxy_async();
           bar_sync(1, 128);
@@ -504,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float alpha = resc ? ex2(m_run - mb) : 1.0f;
 #pragma unroll 1
           for (int h = 0; h < D / 16; ++h) {
+            __syncwarp();
             uint32_t o[16];
             tmem_ld_x16(o_tmem + 16 * h, o);
             ptx::tmem_wait_ld();

@@ -19,7 +19,9 @@ The second model is of the elementwise warps of the dq kernel when a bounded wai
 eight warps meet at barriers that wait without a limit, so whoever gives up has to leave together
 with the others.
 """
+import os
 import random
+import re
 
 import pytest
 
@@ -305,3 +307,26 @@ def test_dq_warps_leave_together(units):
 def test_a_dq_warp_that_leaves_alone_is_caught():
     for units in ([3, 1, 0, 2], [4, 4], [2]):
         assert not all(run_dq_give_up(units, seed, leave_alone=True) for seed in range(2000))
+
+
+def test_warps_converge_ahead_of_reads_of_tmem():
+    """tcgen05.ld takes whole converged warps. In loops that are not unrolled the read follows the
+    stores of the turn before, which lanes without a row or key of their own skip: each such
+    loop begins with a __syncwarp, and no turn is cut short for some lanes."""
+    here = os.path.join(os.path.dirname(__file__), "..", "block_sparse_attention_major_b200", "csrc")
+    loops = 0
+    for name in ("cross_fwd.cu", "cross_bwd.cu"):
+        with open(os.path.join(here, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"#pragma unroll 1\s+for \([^{]*\) \{", text):
+            depth, at = 1, m.end()
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[at], 0)
+                at += 1
+            body = text[m.end():at]
+            if "tmem_ld" not in body or "warp_wait" in body:
+                continue                    # a loop over whole blocks: its waits are votes of the warp
+            loops += 1
+            assert body.split()[0] == "__syncwarp();", (name, m.group(0))
+            assert not re.search(r"if \(key[^)]*\) continue", body), name
+    assert loops == 4
