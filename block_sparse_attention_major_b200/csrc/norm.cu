@@ -537,8 +537,10 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
 // thread mean fewer warps a row, and the reductions, whose cost goes by the warp, are what a
 // block waits for (75600 rows of 5120 with 1 slot and 20 warps: 389 us); registers set the limit:
 // a slot takes 4 (bf16) or 8 of the row and 16 of w and b, or 24 of w, dw and db.
+// `built` is the thread count that the kernel of the launch is compiled for: norm_blocks reckons what
+// is resident on an SM by it, and run_norm takes the kernel by it.
 struct NormShape {
-  int tpr, vpt, threads;
+  int tpr, vpt, threads, built;
 };
 NormShape norm_shape(int C, bool bwd, bool fp32, int run) {
   const int slots = ceil_div(C, 8), most = run == 1 ? 1 : bwd || fp32 || run == 2 ? 2 : 4;
@@ -546,7 +548,7 @@ NormShape norm_shape(int C, bool bwd, bool fp32, int run) {
   if (slots <= 32 * most) {                         // a warp or less
     n.vpt = slots <= 32 ? 1 : slots <= 64 ? 2 : 4;
     n.tpr = slots <= 8 ? 8 : slots <= 16 ? 16 : 32;
-    n.threads = 256;
+    n.threads = n.built = 256;
     return n;
   }
   if (run == 1) {                                    // no copies ahead: as many threads as go
@@ -556,6 +558,8 @@ NormShape norm_shape(int C, bool bwd, bool fp32, int run) {
     if (slots > 1024) n.vpt = 4;
   }
   n.threads = n.tpr = 32 * ceil_div(slots, 32 * n.vpt);
+  if (run == 1) n.built = n.vpt > 1 ? 512 : n.threads > 256 ? 640 : 256;
+  else n.built = n.threads <= 256 ? 256 : n.vpt == 2 && n.threads <= 320 ? 320 : 512;
   return n;
 }
 
@@ -578,8 +582,7 @@ constexpr int per_sm(int vpt, int T, bool bwd, int E) {
 // block's lane groups.
 int norm_blocks(const NormShape& n, long long rows, bool bwd, int run) {
   const long long step = n.threads / n.tpr, need = (rows + step - 1) / step;
-  const int T = n.threads > 320 ? n.threads : n.threads > 256 ? 320 : 256;
-  const long long full = (long long)kNormSms * (per_sm(n.vpt, T, bwd, run) * T / n.threads);
+  const long long full = (long long)kNormSms * (per_sm(n.vpt, n.built, bwd, run) * n.built / n.threads);
   return (int)(need < full ? need : full);
 }
 
@@ -621,12 +624,12 @@ template <typename XT, typename YT, int E>
 cudaError_t run_norm(const NormArgs& a, bool bwd, const NormShape& n, int blocks, cudaStream_t s) {
   // what norm_shape gives for these rows, and nothing else
   if constexpr (E == 1) {
-    if (n.vpt == 1 && n.threads > 256) return run_either<XT, YT, E, 1, 640>(a, bwd, n, blocks, s);
+    if (n.built == 640) return run_either<XT, YT, E, 1, 640>(a, bwd, n, blocks, s);
   } else {
-    if (n.vpt == 2 && n.threads <= 256) return run_either<XT, YT, E, 2, 256>(a, bwd, n, blocks, s);
-    if (n.vpt == 2 && n.threads <= 320) return run_either<XT, YT, E, 2, 320>(a, bwd, n, blocks, s);
+    if (n.vpt == 2 && n.built == 256) return run_either<XT, YT, E, 2, 256>(a, bwd, n, blocks, s);
+    if (n.built == 320) return run_either<XT, YT, E, 2, 320>(a, bwd, n, blocks, s);
     if constexpr (E >= 4 && sizeof(XT) == 2)        // forward only: the backward pass has 4 slots past 256 threads
-      if (n.vpt == 4 && n.threads <= 256) return run_fwd<XT, YT, E, 4, 256>(a, n, blocks, s);
+      if (n.vpt == 4 && n.built == 256) return run_fwd<XT, YT, E, 4, 256>(a, n, blocks, s);
   }
   if (n.vpt == 1) return run_either<XT, YT, E, 1, 256>(a, bwd, n, blocks, s);
   if (n.vpt == 2) return run_either<XT, YT, E, 2, 512>(a, bwd, n, blocks, s);
@@ -678,8 +681,9 @@ cudaError_t dispatch(const bsa_norm_shape& f, NormArgs& a, bool bwd, cudaStream_
 }  // namespace
 
 size_t norm_workspace(const bsa_norm_shape& f) {
-  int blocks = 0;                 // whatever the addresses allow
+  int blocks = 0;                 // whatever the addresses allow of what the width does
   for (const int run : {1, 2, 8}) {
+    if (f.C % run != 0) continue;
     const int n = norm_blocks(norm_shape(f.C, true, f.x_type == BSA_FP32, run), f.rows, true, run);
     if (n > blocks) blocks = n;
   }

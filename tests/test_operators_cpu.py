@@ -179,3 +179,14 @@ def test_forward_norms_through_the_output_buffer(monkeypatch):
     assert names == ["bsa_layer_norm_fwd", "bsa_reorder_pool"] * 2 + ["bsa_reorder", "bsa_build_mask_pooled",
                                                                       "bsa_sparse_attn_fwd"]
     assert calls[0][1][4] == b.out.data_ptr() and calls[1][1][1].value == b.out.data_ptr()
+
+
+@pytest.mark.parametrize("C,blocks", [(2049, 2), (2305, 2), (2559, 2), (4097, 1), (8200, 1), (9000, 1), (10240, 1), (16384, 1)])
+def test_norm_grid_is_what_is_resident(lib, C, blocks):
+    # a partial row for each block and one more: wide rows are read by kernels built for 512 or 640
+    # threads, one block an SM or, with half the threads, two
+    import block_sparse_attention_major_b200 as bsa
+    for xt in (0, 1):
+        f = bsa.bsa_norm_shape(10 ** 6, C, 1, 0, xt, xt, 1, 1e-6, 0.0)
+        n = (148 * blocks + 1) * C * 8
+        assert lib.bsa_layer_norm_workspace_bytes(ctypes.byref(f)) == (n + 255) // 256 * 256
