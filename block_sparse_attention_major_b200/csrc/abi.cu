@@ -9,6 +9,8 @@
 
 #include "common.cuh"
 #include "cross.cuh"
+#include "norm.cuh"
+#include "once.cuh"
 #include "window.cuh"
 
 namespace bsa {

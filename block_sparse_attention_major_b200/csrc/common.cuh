@@ -5,7 +5,6 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <atomic>
 #include <stdint.h>
 
 #include "bsa.h"
@@ -115,26 +114,6 @@ __device__ __forceinline__ int tile_valid_count(const Geom& g, int tt, int ty, i
          min(kTileEdge, g.Ws - tx * kTileEdge);
 }
 
-// Checks something once for each device (of the first 64; each time on others): what a device or a
-// kernel is does not change, and asking again costs a launch's host time.
-class OncePerDevice {
- public:
-  template <typename F>
-  cudaError_t operator()(F&& f) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-    if (bit & done_.load(std::memory_order_acquire)) return cudaSuccess;
-    e = f();
-    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
-    return e;
-  }
-
- private:
-  std::atomic<uint64_t> done_{0};
-};
-
 // ------------------------------------------------------------------ error reporting
 __device__ __forceinline__ void report_error(uint32_t* err, uint32_t bits) {
   if (err) atomicOr(err, bits);
@@ -166,11 +145,5 @@ cudaError_t launch_sparse_attn_fixed_scratch(const Geom& g, const __nv_bfloat16*
                                              const __nv_bfloat16* vt, const uint32_t* mask,
                                              const int32_t* kv_count, float scale, __nv_bfloat16* out,
                                              float* lse, uint32_t* errors, cudaStream_t s);
-size_t norm_workspace(const bsa_norm_shape& f);
-cudaError_t launch_norm_fwd(const bsa_norm_shape& f, const void* x, const void* w, const void* b, void* y,
-                            float* mean, float* rstd, cudaStream_t s);
-cudaError_t launch_norm_bwd(const bsa_norm_shape& f, const void* x, const void* dy, const float* mean,
-                            const float* rstd, const void* w, void* dx, float* dw, float* db, void* ws,
-                            cudaStream_t s);
 void count_launches(int n);
 }  // namespace bsa

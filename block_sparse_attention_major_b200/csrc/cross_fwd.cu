@@ -34,6 +34,7 @@
 // maximum to exponentials to P V to the next scores, some 2000 cycles of softmax and 1100 to 1400
 // of products for a key tile, of which two blocks hide half; with few key tiles, the change of units.
 #include "cross.cuh"
+#include "once.cuh"
 
 #include <math.h>
 

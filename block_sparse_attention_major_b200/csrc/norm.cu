@@ -29,8 +29,8 @@
 // 109 and 196 us (5.6 and 5.1 TB/s); 393120 rows of 128 bf16 47 and 80 us (4.3 and 3.8 TB/s; fewer
 // bytes a reduction, not profiled); the even width 5450 2.4 and 3.0 TB/s; odd widths (1001, 1537,
 // 4097) 0.9 to 1.4 TB/s, single elements without copies ahead.
-#include "common.cuh"
 #include "f32x2.cuh"
+#include "norm.cuh"
 
 namespace bsa {
 namespace {

@@ -65,3 +65,10 @@ def test_reference_arm_prints_a_contract_line():
         assert key in line, key
     assert line["impl"] == "reference" and line["value"] > 0 and line["steps"] == 3
     assert line["e2e"]["h2d_bytes_per_step"] == 0 and line["cpu_baseline"]["kind"] == "oracle"
+
+
+@pytest.mark.parametrize("workload", ["hunyuan", "wan13b"])
+def test_traffic_figure_belongs_to_this_attention_kernel(workload):
+    # the committed capture counts only for the sources that it was taken of
+    traffic, source = bench._traffic(workload)
+    assert traffic and source.startswith("ncu"), source
