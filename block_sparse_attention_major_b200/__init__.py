@@ -776,6 +776,12 @@ class CrossBuffers:
         self.ws = alloc_cross_workspace(g, dev)
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two contiguous tensors share memory."""
+    lo, hi = a.data_ptr(), b.data_ptr()
+    return lo < hi + b.numel() * b.element_size() and hi < lo + a.numel() * a.element_size()
+
+
 def cross_forward(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                   kv_len: torch.Tensor | None = None, key_mask: torch.Tensor | None = None,
                   qk_norm: QKNorm | None = None, bufs: CrossBuffers | None = None, scale: float | None = None,
@@ -811,18 +817,24 @@ def forward(g: Geometry, p: MaskParams, q: torch.Tensor, k: torch.Tensor, v: tor
     attention masks the tokens outside each query token's support inside window tiles,
     with the route flags the mask build left in the workspace.
     qk_norm: layer norm of Q and K over the head dimension first (the mask is then that of the
-    normalised Q and K).
+    normalised Q and K). q, k and v may be the `out` of an earlier call on these buffers.
     """
     if not rebuild_mask and bufs is None:
         raise ValueError("rebuild_mask=False attends through the mask held in bufs: pass the "
                          "Buffers of an earlier call")
     b = bufs or Buffers(g, q.device)
-    for x, xt, xbar, norm in ((q, b.qt, b.qbar, qk_norm and (qk_norm.q_weight, qk_norm.q_bias)),
-                              (k, b.kt, b.kbar, qk_norm and (qk_norm.k_weight, qk_norm.k_bias))):
+    # The normalised Q and K pass through `out`, which is not written before V has been reordered; or,
+    # where an input lies there, through the tile-major buffer that is filled next.
+    taken = False
+    if qk_norm is not None:
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            _need(t, torch.bfloat16, (g.B, g.N, g.H, g.d), name)
+            taken |= _overlap(t, b.out)
+    for x, xt, xbar, norm, free in ((q, b.qt, b.qbar, qk_norm and (qk_norm.q_weight, qk_norm.q_bias), b.kt),
+                                    (k, b.kt, b.kbar, qk_norm and (qk_norm.k_weight, qk_norm.k_bias), b.vt)):
         if qk_norm is not None:
-            # through `out`, which is not written before both have been reordered
-            _need(x, torch.bfloat16, (g.B, g.N, g.H, g.d), "q and k")
-            x, _, _ = layer_norm_fwd(x, *norm, qk_norm.eps, y=b.out, want_stats=False, stream=stream)
+            y = free.view(-1)[:x.numel()].view(x.shape) if taken else b.out
+            x, _, _ = layer_norm_fwd(x, *norm, qk_norm.eps, y=y, want_stats=False, stream=stream)
         if rebuild_mask:
             reorder_pool(g, x, xt, xbar, stream)
         else:

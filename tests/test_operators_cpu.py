@@ -190,3 +190,25 @@ def test_norm_grid_is_what_is_resident(lib, C, blocks):
         f = bsa.bsa_norm_shape(10 ** 6, C, 1, 0, xt, xt, 1, 1e-6, 0.0)
         n = (148 * blocks + 1) * C * 8
         assert lib.bsa_layer_norm_workspace_bytes(ctypes.byref(f)) == (n + 255) // 256 * 256
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_forward_with_norms_leaves_inputs_in_the_output_buffer_alone(monkeypatch, which):
+    import types
+    import block_sparse_attention_major_b200 as bsa
+    calls = []
+    fake(monkeypatch, bsa, calls)
+    monkeypatch.setattr(bsa, "_norm_shape", lambda *a: bsa.bsa_norm_shape(1, 64, 1, 0, 0, 0, 1, 1e-6, 0.0))
+    g, p = bsa.Geometry(1, 2, 64, 5, 6, 7), bsa.MaskParams(1, 1)
+    x = [torch.zeros(g.B, g.N, g.H, g.d, dtype=torch.bfloat16) for _ in range(3)]
+    tiled = lambda: torch.zeros(g.B, g.H, g.NT, 64, g.d, dtype=torch.bfloat16)
+    b = types.SimpleNamespace(**{n: torch.zeros(8) for n in ("qbar", "kbar", "mask", "kv_count", "lse")}, qt=tiled(),
+                              kt=tiled(), vt=tiled(), out=x[which], ws=torch.zeros(4096, dtype=torch.uint8))
+    w = torch.ones(64)
+    bsa.forward(g, p, *x, torch.zeros(1, g.NT), bufs=b, qk_norm=bsa.QKNorm(w, w, w, w))
+    norms = [c[1] for c in calls if c[0] == "bsa_layer_norm_fwd"]
+    pools = [c[1] for c in calls if c[0] == "bsa_reorder_pool"]
+    assert [n[1] for n in norms] == [x[0].data_ptr(), x[1].data_ptr()]
+    # Q through the place of the tiled K, K through that of V, each before it is filled
+    assert [n[4] for n in norms] == [b.kt.data_ptr(), b.vt.data_ptr()] == [q[1].value for q in pools]
+    assert [q[2].value for q in pools] == [b.qt.data_ptr(), b.kt.data_ptr()]

@@ -109,3 +109,23 @@ def test_block_with_its_gradients_in_one_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(held, step()))
+
+
+def test_forward_with_qk_norm_of_an_earlier_output():
+    import block_sparse_attention_major_b200 as bsa
+    for name in ("ragged128", "token128"):
+        w, q, k, v, diff = C.inputs(name)
+        g, p = C.geometry(w), C.params(w)
+        q, k, v, diff = (t.cuda() for t in (q, k, v, diff))
+        gen = torch.Generator().manual_seed(2)
+        norm = bsa.QKNorm(*(torch.randn((w.d,), generator=gen).cuda() for _ in range(4)))
+        for i in range(3):
+            bufs = bsa.forward(g, p, q, k, v, diff)
+            x = [q, k, v]
+            x[i] = bufs.out.clone()
+            want = bsa.forward(g, p, *x, diff, qk_norm=norm)
+            x[i] = bufs.out
+            got = bsa.forward(g, p, *x, diff, bufs=bufs, qk_norm=norm)
+            torch.cuda.synchronize()
+            assert bsa.read_error(got.ws) == 0
+            assert torch.equal(got.mask, want.mask) and torch.equal(got.out, want.out), "qkv"[i]
