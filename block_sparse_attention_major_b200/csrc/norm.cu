@@ -422,10 +422,12 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
           const uint64_t nm = f2(-m[u], -m[u]), r2 = f2(rs[u], rs[u]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            // past the row's end dy is zero, so none of the sums sees the element
-            const uint64_t d = gs[u][k].pair(i), h = fmul2(fadd2(xs[u][k].pair(i), nm), r2), g = fmul2(d, w[k][i]);
+            // Past the row's end dy is zero, so neither sum sees the element: sum g h is taken as
+            // rstd sum g (x - mean), since h = (0 - mean) rstd may be infinite there where the row's
+            // own are not.
+            const uint64_t d = gs[u][k].pair(i), e = fadd2(xs[u][k].pair(i), nm), h = fmul2(e, r2), g = fmul2(d, w[k][i]);
             s1[u] = fadd2(s1[u], g);
-            s2[u] = ffma2(g, h, s2[u]);
+            s2[u] = ffma2(g, e, s2[u]);
             dw[k][i] = ffma2(d, h, dw[k][i]);
             db[k][i] = fadd2(db[k][i], d);
           }
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(T, kPerSm) norm_bwd_kernel(NormArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const long long r = base + u * rpb + sub;
-          const float c1 = s[2 * u] * inv_c, c2 = s[2 * u + 1] * inv_c;
+          const float c1 = s[2 * u] * inv_c, c2 = s[2 * u + 1] * rs[u] * inv_c;
           const uint64_t nm = f2(-m[u], -m[u]), r2 = f2(rs[u], rs[u]), n1 = f2(-c1, -c1), n2 = f2(-c2, -c2);
           float o[8];
 #pragma unroll

@@ -297,3 +297,20 @@ def test_many_items_a_block(C):
             h = (x.double() - mean.double()[..., None]) * rstd.double()[..., None]
             near(dw, (dy.double() * h).sum(1).cpu(), (dy.double() * h).abs().sum(1).cpu(), "dweight")
             near(db, dy.double().sum(1).cpu(), dy.double().abs().sum(1).cpu(), "dbias")
+
+
+@pytest.mark.parametrize("C", [4, 32, 520, 1032, 33, 30])
+def test_places_past_a_row_of_large_equal_values(C):
+    # mean 2^118 and rstd 2^10: (0 - mean) rstd is past fp32, and only places past the row's end see it.
+    # h is 0 in the row, so dx = rstd (g - mean g), dw = 0 and db = dy.
+    import block_sparse_attention_major_b200 as bsa
+    eps = 2.0 ** -20
+    x = torch.full((3, C), 2.0 ** 118, device="cuda")
+    dy = torch.randn((3, C), generator=torch.Generator().manual_seed(70)).cuda()
+    w = torch.ones(C, device="cuda")
+    mean, rstd = torch.full((3,), 2.0 ** 118, device="cuda"), torch.full((3,), eps ** -0.5, device="cuda")
+    dx, dw, db = bsa.layer_norm_bwd(x, dy, mean, rstd, w)
+    g = dy.double().cpu()
+    near(dx, 2.0 ** 10 * (g - g.mean(1, keepdim=True)), 2.0 ** 10 * (g.abs() + g.abs().mean(1, keepdim=True)), "dx", half_step(F32))
+    assert not dw.any()
+    near(db, g.sum(0), g.abs().sum(0), "dbias")
