@@ -136,6 +136,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.bsa_launch_count.argtypes = []
         lib.bsa_selftest_bounded_wait.restype = ctypes.c_int
         lib.bsa_selftest_bounded_wait.argtypes = [ctypes.c_longlong, vp, vp]
+        lib.bsa_selftest_cross_wait.restype = ctypes.c_int
+        lib.bsa_selftest_cross_wait.argtypes = [vp, vp]
         if path is None:
             _lib = lib
         return lib
@@ -285,6 +287,14 @@ def selftest_bounded_wait(err: torch.Tensor, limit_cycles: int = 20_000_000, str
     _need(err, torch.int32, (1,), "err")
     _run("bsa_selftest_bounded_wait", err.device, stream,
          lambda s: load_library().bsa_selftest_bounded_wait(ctypes.c_longlong(limit_cycles), _ptr(err), s))
+
+
+def selftest_cross_wait(err: torch.Tensor, stream=None) -> None:
+    """Run the self-test of the cross attention's bounded wait: half the warps of a group wait for an
+    arrival that never comes, give up and take the others with them; KERR_WAIT_TIMEOUT in err
+    (int32 [1], device), KERR_BAD_UNIT where a thread was told to carry on."""
+    _need(err, torch.int32, (1,), "err")
+    _run("bsa_selftest_cross_wait", err.device, stream, lambda s: load_library().bsa_selftest_cross_wait(_ptr(err), s))
 
 
 def reorder(g: Geometry, x: torch.Tensor, xt: torch.Tensor | None = None, stream=None) -> torch.Tensor:

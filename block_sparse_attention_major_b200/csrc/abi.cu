@@ -160,6 +160,7 @@ using namespace bsa;
 
 namespace bsa {
 cudaError_t launch_wait_selftest(long long limit_cycles, uint32_t* err, cudaStream_t s);   // selftest.cu
+cudaError_t launch_cross_wait_selftest(uint32_t* err, cudaStream_t s);
 }
 
 extern "C" {
@@ -397,6 +398,14 @@ int bsa_selftest_bounded_wait(long long limit_cycles, uint32_t* err, void* strea
   const int dev = device_ok();
   if (dev != BSA_OK) return dev;
   return status_of(bsa::launch_wait_selftest(limit_cycles, err, static_cast<cudaStream_t>(stream)));
+}
+
+int bsa_selftest_cross_wait(uint32_t* err, void* stream) {
+  const CallRange range("bsa_selftest_cross_wait");
+  if (!err || (reinterpret_cast<uintptr_t>(err) & 3u) != 0) return BSA_ERR_INVALID_ARG;
+  const int dev = device_ok();
+  if (dev != BSA_OK) return dev;
+  return status_of(bsa::launch_cross_wait_selftest(err, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

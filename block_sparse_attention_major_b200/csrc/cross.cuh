@@ -113,10 +113,11 @@ namespace cross {
 // stands at every hand-over of warps that run little else: with a clock in it, the code of the
 // waits alone displaced the others' from the instruction cache.
 constexpr int kWaitTries = 1 << 25;
+template <int kTries = kWaitTries>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
-  for (int i = 0; i < kWaitTries; ++i) {
+  for (int i = 0; i < kTries; ++i) {
     if (ptx::mbar_try_wait_ns(bar, parity, 200)) return true;
     if (*abort) return false;
   }
@@ -140,8 +141,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 // All lanes take the same decision after a per-thread bounded wait.
+template <int kTries = kWaitTries>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  return __all_sync(0xffffffffu, wait_phase(bar, parity, abort, err));
+  return __all_sync(0xffffffffu, wait_phase<kTries>(bar, parity, abort, err));
 }
 
 // Box of a 4-D map (columns, heads, tokens, items) into shared memory.

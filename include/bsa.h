@@ -367,6 +367,12 @@ uint64_t bsa_launch_count(void);
  * null or misaligned err or an out-of-range limit. */
 int bsa_selftest_bounded_wait(long long limit_cycles, uint32_t* err, void* stream);
 
+/* The same for the bounded wait of the cross-attention kernels, whose limit is a number of tries
+ * (here 4096, below a millisecond): half the warps of a group wait for an arrival that never comes,
+ * the others for one that has, and all of them leave together by a vote. Sets
+ * BSA_KERR_WAIT_TIMEOUT in *err, and BSA_KERR_BAD_UNIT where a thread was told to carry on. */
+int bsa_selftest_cross_wait(uint32_t* err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

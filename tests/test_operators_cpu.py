@@ -212,3 +212,8 @@ def test_forward_with_norms_leaves_inputs_in_the_output_buffer_alone(monkeypatch
     # Q through the place of the tiled K, K through that of V, each before it is filled
     assert [n[4] for n in norms] == [b.kt.data_ptr(), b.vt.data_ptr()] == [q[1].value for q in pools]
     assert [q[2].value for q in pools] == [b.qt.data_ptr(), b.kt.data_ptr()]
+
+
+def test_cross_wait_selftest_arguments_refused(lib):
+    assert lib.bsa_selftest_cross_wait(None, None) == 1
+    assert lib.bsa_selftest_cross_wait(ctypes.c_void_p(P + 2), None) == 1
