@@ -20,6 +20,9 @@ Entry points (same names as the C ABI in include/bsa.h):
     cross_forward(g, q, k, v, ..., qk_norm)  the norm of Q and K per head, then that attention
     layer_norm_fwd(x, weight, bias)          -> (y, mean, rstd), over the last axis
     layer_norm_bwd(x, dy, mean, rstd, weight)    -> (dx, dweight, dbias)
+
+No call takes part in autograd: outputs have no grad_fn, whatever the inputs require. Gradients
+are those that the _bwd calls return.
 """
 from __future__ import annotations
 
@@ -578,7 +581,8 @@ def cross_attn_fwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.
     may be passed as they are, and k and v expanded over the items).
 
     kv_len (int32 [B]) and key_mask (bool [B,M]) say which keys of an item are valid; an item
-    without one gives 0 and an lse of -inf. Returns (out bf16 [B,N,H,d], lse fp32 [B,H,N])."""
+    without one gives 0 and an lse of -inf. scale: finite, above 0. Outputs may not overlap inputs.
+    Returns (out bf16 [B,N,H,d], lse fp32 [B,H,N])."""
     st = _cross_inputs(g, q, k, v, kv_len, key_mask)
     out = _given(out, q, torch.bfloat16, (g.B, g.N, g.H, g.d), "out", stream)
     if want_lse or lse is not None:
@@ -597,8 +601,9 @@ def cross_attn_bwd(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.
                    dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
                    ws: torch.Tensor | None = None,
                    stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    """Gradients of cross_attn_fwd from its inputs, its out and lse, and dout: dq [B,N,H,d], and dk
-    and dv [B,M,Hkv,d] per item, zero at keys that are not valid (all bf16)."""
+    """Gradients of cross_attn_fwd from its inputs, its out and lse, and dout (contiguous): dq [B,N,H,d],
+    and dk and dv [B,M,Hkv,d] per item, zero at keys that are not valid (all bf16). Outputs may not
+    overlap inputs."""
     st = _cross_inputs(g, q, k, v, kv_len, key_mask)
     _need(out, torch.bfloat16, (g.B, g.N, g.H, g.d), "out")
     _need(dout, torch.bfloat16, (g.B, g.N, g.H, g.d), "dout")
@@ -685,7 +690,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
 
     weight, bias: absent, [C], or [x.shape[0], C] (one row per batch item, as the modulation of
     a diffusion transformer; weight_offset=1 where it is stored as the distance from one).
-    Returns y (out_dtype, x's type unless given) and the fp32 mean and rstd of every row for
+    y may be x itself where the types agree. Returns y (out_dtype, x's type unless given) and the fp32 mean and rstd of every row for
     the backward pass (None without want_stats)."""
     dt = y.dtype if y is not None and out_dtype is None else out_dtype or getattr(x, "dtype", None)
     f = _norm_shape(x, dt, weight, bias, eps, weight_offset)
@@ -717,8 +722,9 @@ def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: 
                    want_bias: bool = True, dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
                    dbias: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                    stream=None) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor | None]:
-    """Gradients of layer_norm_fwd: dx (x's type), and dweight and dbias in float32, of the
-    weight's shape (None without a weight, or where they are not wanted)."""
+    """Gradients of layer_norm_fwd from x, dy (both contiguous) and its statistics: dx (x's type; may
+    be x or dy itself where the types agree), and dweight and dbias in float32, of the weight's
+    shape (None without a weight, or where they are not wanted)."""
     f = _norm_shape(x, getattr(dy, "dtype", None), weight, None, 0.0, weight_offset)
     _need(dy, dy.dtype, x.shape, "dy")
     _need(mean, torch.float32, x.shape[:-1], "mean")
@@ -765,7 +771,8 @@ class Buffers:
 @dataclass(frozen=True)
 class QKNorm:
     """Layer norm of Q and K over the head dimension ahead of attention: weights and biases [d]
-    (bfloat16 or float32), shared by all heads and tokens; None for none."""
+    (bfloat16 or float32), shared by all heads and tokens; None for none. Models that normalise Q
+    and K by their root mean square need a norm of their own ahead of the call."""
 
     q_weight: torch.Tensor | None = None
     q_bias: torch.Tensor | None = None
@@ -798,7 +805,8 @@ def cross_forward(g: CrossGeometry, q: torch.Tensor, k: torch.Tensor, v: torch.T
                   stream=None) -> CrossBuffers:
     """The attention to an encoder's states as a block runs it: the norm of Q and K per head, if
     any (q and k are then contiguous), and cross_attn_fwd. Returns the buffers; out and lse hold
-    the result."""
+    the result. The way back is made of cross_attn_bwd on qn and kn and of layer_norm_bwd, for which
+    layer_norm_fwd gives the statistics of q and k."""
     if bufs is None:
         with _owned_by(stream):
             bufs = CrossBuffers(g, qk_norm is not None, q.device)

@@ -26,9 +26,9 @@
 // Roundings to fewer bits: P and dS to bf16 ahead of their products, the gradients once.
 //
 // Measured, one B200, 32760 queries, 512 keys, 12 heads of 128: statistics 42 us (4.8 TB/s), dq 155 us
-// (1.0 PFLOP/s of the 6 N M H d that it runs; the tensor pipe 47 % busy, the rest is the chain from T
-// through dS to the next T and the change of units), dk and dv 165 us (1.25 PFLOP/s of 8 N M H d, 66 %
-// busy; its products read 128 bytes a cycle from shared memory, all there is, and every copy of Q
+// (1.0 PFLOP/s of the 6 N M H d that it runs; profiled by itself 171 us, the tensor pipe 48 % busy, the
+// rest is the chain from T through dS to the next T and the change of units), dk and dv 165 us (1.25
+// PFLOP/s of 8 N M H d; by itself 176 us, 66 % busy; its products read 128 bytes a cycle from shared memory, all there is, and every copy of Q
 // and dO takes some of it), the join 8 us. Over 4096 keys 1.13 to 1.25 and 1.3 PFLOP/s (two passes).
 #include "cross.cuh"
 

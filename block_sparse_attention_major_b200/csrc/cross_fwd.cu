@@ -28,8 +28,8 @@
 // Roundings to fewer bits: P to bf16 for the P V product, the output once. The sum of a row is
 // that of the unrounded probabilities.
 //
-// Measured, one B200, 12 heads of 128: 32760 queries over 512 keys 110 us (0.93 PFLOP/s; the tensor
-// pipe 46 % busy, DRAM 16 %), over 4096 keys 706 and 788 us in two passes (1.17 and 1.05 PFLOP/s),
+// Measured, one B200, 12 heads of 128: 32760 queries over 512 keys 110 us (0.93 PFLOP/s; profiled by
+// itself, with cold caches, 123 us, the tensor pipe 47 % busy, DRAM 16 %), over 4096 keys 706 and 788 us in two passes (1.17 and 1.05 PFLOP/s),
 // over 128 keys 52 us (0.5 PFLOP/s, 3.9 TB/s). What bounds it is the chain of a block, scores to
 // maximum to exponentials to P V to the next scores, some 2000 cycles of softmax and 1100 to 1400
 // of products for a key tile, of which two blocks hide half; with few key tiles, the change of units.

@@ -24,11 +24,13 @@
 // the partials of an item in the order of the blocks. No atomics: repeated calls give
 // identical bits.
 //
-// Measured, one B200, two passes alike: 75600 x 5120 bf16 forward 298 us (5.2 TB/s of the 6.6 that a
-// copy reaches), backward with the weight's gradient 462 us (5.0 TB/s); 65520 x 1536, fp32 to bf16,
-// 109 and 196 us (5.6 and 5.1 TB/s); 393120 rows of 128 bf16 47 and 80 us (4.3 and 3.8 TB/s; fewer
-// bytes a reduction, not profiled); the even width 5450 2.4 and 3.0 TB/s; odd widths (1001, 1537,
-// 4097) 0.9 to 1.4 TB/s, single elements without copies ahead.
+// Measured, one B200, two passes alike: 75600 x 5120 bf16 forward 285 us (5.4 TB/s of the 6.6 that a
+// copy reaches), backward with the weight's gradient 463 us (5.0 TB/s); 65520 x 1536, fp32 to bf16,
+// 108 and 198 us (5.6 and 5.1 TB/s); 393120 rows of 128 bf16 46 and 81 us (4.3 and 3.7 TB/s; fewer
+// bytes a reduction: the forward pass has 72 % of its issue slots busy, the backward pass 45 %); the
+// even width 5450 2.4 and 2.8 TB/s; odd widths 0.9 to 1.2 TB/s forward (1001, 1537, 2049 to 2559, 4097)
+// and 0.9 to 1.6 backward, single elements without copies ahead; 8200 to 10240 bf16 3.3 to 4.0 and
+// 1.8 to 1.9 TB/s.
 #include "f32x2.cuh"
 #include "norm.cuh"
 
@@ -573,9 +575,13 @@ constexpr int kFwdU = E == 1 ? 1 : VPT == 1 ? 8 / sizeof(XT) : VPT == 2 ? 4 / si
 template <int E, int VPT>
 constexpr int kBwdU = E > 1 && VPT == 1 ? 2 : 1;
 
-// Blocks an SM that a kernel is built for: registers to hold everything (what does not fit goes
+// Blocks an SM that a kernel is built for: registers to hold nearly everything (what does not fit goes
 // through L2, since the copies ahead leave L1 little: a backward pass with 216 bytes of it a
-// thread took twice as long).
+// thread took twice as long). What is left of it: some 60 to 120 bytes a thread in the backward
+// form of 320 threads, up to 30 forward, 460 to 1120 in the backward forms of four slots (widths
+// above 8192) and 660 forward where such a width is odd. Two blocks an SM end at 320 threads, 5120
+// elements at two slots a thread: wider rows have 9 to 16 warps an SM, and no second form was
+// measured for them.
 constexpr int per_sm(int vpt, int T, bool bwd, int E) {
   return T > 320 ? 1 : vpt > 1 ? 2 : (bwd ? 2 : 3) + (E == 1 ? 1 : 0);
 }

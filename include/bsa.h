@@ -335,6 +335,7 @@ size_t bsa_cross_workspace_bytes(const bsa_cross_geom* g);
  *              keys that both allow
  *   out      : bf16 [B, N, H, d];  lse : fp32 [B, H, N], natural log of the sum of exponentials; may be
  *              NULL
+ *   softmax_scale : finite, above 0
  * An item without a valid key gives out = 0 and lse = -inf. What k and v hold at keys that are not
  * valid does not matter (infinities and NaN included). fp32 scores and statistics, bf16
  * probabilities into the P.V product, fp32 accumulation. Deterministic. */
